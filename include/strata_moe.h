@@ -139,6 +139,60 @@ strata_status strata_moe_route(strata_moe_t h, const void *x_dev, int T, int32_t
 strata_status strata_moe_forward(strata_moe_t h, const void *x_dev, int T, void *y_dev,
                                  void *stream);
 
+/* ---- Routing rules.
+ * A rule says how a token's picks and weights follow from its logits l_e:
+ *   score    s_e = softmax over all experts, or 1 / (1 + exp(-l_e)) of each
+ *   value    v_e = s_e + b_e, b the selection bias (it selects and never
+ *            weighs); without a bias the values are in the logits' order
+ *   groups   n_groups equal runs of expert ids; a group counts by its best
+ *            value, or by the sum of its best two (of scores when there is no
+ *            bias); the top_groups best stay, a tie going to the lower group
+ *   picks    the k largest values of the groups that stay, in descending
+ *            order, a tie going to the lower expert id
+ *   weights  s_j of the picks, divided by their sum when renorm, times scale
+ * Values are ordered as 64-bit arithmetic orders them.  An expert with a logit
+ * of -inf or NaN, or a bias of -inf or NaN, is not eligible: it adds nothing
+ * to its group, and where fewer than k eligible experts stay, the other picks
+ * are the lowest remaining ids with weight 0 (so picks are always k different
+ * valid ids).  A logit of +inf counts as the largest finite float. */
+enum { STRATA_SCORE_SOFTMAX = 0, STRATA_SCORE_SIGMOID = 1 };
+enum { STRATA_GROUP_BEST = 0, STRATA_GROUP_SUM2 = 1 };
+/* Element types of caller buffers that may have either. */
+enum { STRATA_BF16 = 0, STRATA_F32 = 1 };
+typedef struct {
+    int32_t score;       /* STRATA_SCORE_* */
+    int32_t n_groups;    /* 1: no groups; divides the number of experts, <= 32 */
+    int32_t top_groups;  /* 1 <= top_groups <= n_groups; their experts number >= k */
+    int32_t group_score; /* STRATA_GROUP_*; SUM2 needs groups of at least two */
+    int32_t renorm;      /* 1: weights divided by their sum over the picks */
+    float scale;         /* factor on every weight; finite */
+} strata_moe_routing;
+
+/* Picks and weights from logits that are already there, without a handle.
+ *   logits_dev      [T][ld] (device), the first E of every row read; bf16 or
+ *                   float as logits_type says; ld >= E
+ *   select_bias_dev float [E] (device) or NULL
+ *   idx_dev int32 [T][k], w_dev float [T][k] out (device)
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32).  Runs on the device that holds
+ * logits_dev, whichever is current; `stream` belongs to that device.  No
+ * workspace: calls on different streams may overlap.  T == 0 is a no-op. */
+strata_status strata_moe_route_logits(const strata_moe_routing *rule, const void *logits_dev,
+                                      int logits_type, int64_t ld, const float *select_bias_dev,
+                                      int T, int E, int k, int32_t *idx_dev, float *w_dev,
+                                      void *stream);
+
+/* Give a layer a routing rule: later strata_moe_route, strata_moe_forward,
+ * strata_moe_forward_host and strata_moe_stack_forward calls pick and weigh by
+ * it (the logits stay the fixed-order fp32 ones, router bias included).
+ *   rule         NULL: back to the rule a new handle has (softmax, no groups,
+ *                no selection bias, weights renormalised over the picks)
+ *   select_bias  float [E] (host, copied) or NULL
+ * Synchronous: waits for the device's work first.  A CUDA graph captured from
+ * the handle earlier keeps the rule it was captured with but reads the
+ * handle's current selection bias: capture again after a change. */
+strata_status strata_moe_set_routing(strata_moe_t h, const strata_moe_routing *rule,
+                                     const float *select_bias);
+
 /* End-to-end forward from host memory: copies x_host (bf16 [T][H]) to the
  * device, runs strata_moe_forward, copies the result to y_host (bf16 [T][H])
  * and synchronises `stream` before returning.  Pinned host buffers make the
@@ -151,6 +205,57 @@ strata_status strata_moe_forward_host(strata_moe_t h, const void *x_host, int T,
  * r = 1/sqrtf(ss/H + 1e-6f), ss = fp32 sum of squares in the router's order.
  *   h_dev, xn_dev bf16 [T][H] (device); may not overlap. */
 strata_status strata_moe_rmsnorm(const void *h_dev, void *xn_dev, int T, int H, void *stream);
+
+/* ---- 8-bit rows.
+ * A row of H values as H one-byte codes and a float scale for every `group`
+ * columns (32, 64 or 128, dividing H; 0: one scale for the row); a code q of
+ * a group with scale s stands for q s.
+ *   STRATA_Q8_E4M3  OCP e4m3 codes, largest magnitude 448
+ *   STRATA_Q8_INT8  two's complement -127 .. 127
+ * A group's scale is (its largest magnitude) / 448 or / 127, its codes the
+ * values divided by that, rounded to nearest even.  A group whose largest
+ * magnitude is below 2^-116 has scale 0 and codes 0; a group that holds an
+ * infinity or a NaN has scale NaN and codes 0, so all of it reads as NaN. */
+enum { STRATA_Q8_E4M3 = 0, STRATA_Q8_INT8 = 1 };
+
+/* A block's pre-norm in one pass: residual addition, weighted RMSNorm, and the
+ * normalised row in bf16, in 8 bits, or both.
+ *   h = bf16(f32(x) + f32(delta));  r = 1 / sqrt(mean(h^2) + eps);
+ *   y = h r weight (fp32);  xn = bf16(y);  (q, scale) = 8-bit row of y
+ *   x_dev      bf16 [T][H]
+ *   delta_dev  bf16 [T][H] or NULL (then h = x)
+ *   weight_dev [H], bf16 or float as weight_type says, or NULL (then 1)
+ *   h_out_dev  bf16 [T][H] out, may be x_dev itself; needed with delta_dev,
+ *              may be NULL without
+ *   xn_dev     bf16 [T][H] out or NULL
+ *   q_dev      uint8 [T][q_stride] out or NULL (q8, group and the strides are
+ *              then not read); scale_dev float [T][scale_stride] out.  Bytes
+ *              past H and scales past the row's groups are left as they are,
+ *              so codes and scales may share one packed row of
+ *              q_stride = 4 * scale_stride bytes.
+ * Squares are summed in fp32, in 64 bits when the sum leaves its range.  H a multiple of 32 up to 16384; pointers
+ * 16-byte aligned (scale_dev and a float weight_dev included), q_stride a
+ * multiple of 16; eps >= 0.  Other overlaps of outputs with anything are
+ * refused.  Runs on the device that holds x_dev; no workspace. */
+strata_status strata_moe_add_rmsnorm(const void *x_dev, const void *delta_dev,
+                                     const void *weight_dev, int weight_type, float eps, int T,
+                                     int H, void *h_out_dev, void *xn_dev, int q8, int group,
+                                     void *q_dev, int64_t q_stride, float *scale_dev,
+                                     int64_t scale_stride, void *stream);
+
+/* Read 8-bit rows back: out row i = bf16(q s) of row rows[i].
+ *   q_dev uint8 [n_src][q_stride], scale_dev float [n_src][scale_stride] as
+ *   strata_moe_add_rmsnorm writes them
+ *   rows_dev  int32 [n] (device) or NULL (row i itself; n <= n_src); a row
+ *             outside [0, n_src) is skipped, its output row left as it is
+ *   out_dev   bf16 [n][H] out
+ * H a multiple of 32; q_dev and out_dev 16-byte aligned, scale_dev 4-byte,
+ * q_stride a multiple of 16.  Runs on the device that holds q_dev; no
+ * workspace. */
+strata_status strata_moe_dequant_rows(const void *q_dev, int q8, int64_t q_stride,
+                                      const float *scale_dev, int64_t scale_stride, int group,
+                                      const int32_t *rows_dev, int n, int n_src, int H,
+                                      void *out_dev, void *stream);
 
 /* 48-layer-style expert stack, in place: for each layer l in order,
  * h <- bf16(f32(h) + f32(MoE_l(RMSNorm(h)))).

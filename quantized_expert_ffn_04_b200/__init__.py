@@ -27,6 +27,10 @@ _lib = C.CDLL(LIB_PATH)
 STRATA_OK, STRATA_ERR_INVALID_ARG, STRATA_ERR_UNSUPPORTED, STRATA_ERR_OOM, STRATA_ERR_CUDA, \
     STRATA_ERR_TIMEOUT, STRATA_ERR_BOUNDS = range(7)
 STRATA_OPT_PATH, STRATA_OPT_WAIT_BUDGET, STRATA_OPT_DECODE_MAX_T = 1, 2, 3
+STRATA_SCORE_SOFTMAX, STRATA_SCORE_SIGMOID = 0, 1
+STRATA_GROUP_BEST, STRATA_GROUP_SUM2 = 0, 1
+STRATA_BF16, STRATA_F32 = 0, 1
+STRATA_Q8_E4M3, STRATA_Q8_INT8 = 0, 1
 
 # every symbol the header declares
 SYMBOLS = ("strata_moe_create", "strata_moe_destroy", "strata_moe_route", "strata_moe_forward",
@@ -36,7 +40,9 @@ SYMBOLS = ("strata_moe_create", "strata_moe_destroy", "strata_moe_route", "strat
            "strata_moe_set_probe", "strata_moe_launch_count", "strata_moe_route_noalloc",
            "strata_moe_debug_fail_alloc", "strata_moe_debug_live_allocs",
            "strata_ep_expert_range", "strata_ep_plan", "strata_ep_gather_rows",
-           "strata_moe_expert_rows", "strata_moe_combine_rows", "strata_moe_debug_screen")
+           "strata_moe_expert_rows", "strata_moe_combine_rows", "strata_moe_debug_screen",
+           "strata_moe_route_logits", "strata_moe_set_routing", "strata_moe_add_rmsnorm",
+           "strata_moe_dequant_rows")
 
 
 class strata_moe_config(C.Structure):
@@ -49,6 +55,11 @@ class strata_moe_weights(C.Structure):
     _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("router_w", C.c_void_p),
                 ("router_b", C.c_void_p), ("shared_codes", C.c_void_p),
                 ("shared_scales", C.c_void_p)]
+
+
+class strata_moe_routing(C.Structure):
+    _fields_ = [("score", C.c_int32), ("n_groups", C.c_int32), ("top_groups", C.c_int32),
+                ("group_score", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float)]
 
 
 class StrataError(RuntimeError):
@@ -80,6 +91,12 @@ _sig = {
     "strata_ep_gather_rows": [_P, _P, _I, _I, _I, _P, _P],
     "strata_moe_expert_rows": [_P, _P, _P, _I, _I, _I, _P, _P, _P],
     "strata_moe_combine_rows": [_P, _P, _I, _P, _P, _P, _P, _I, _P, _P],
+    "strata_moe_route_logits": [C.POINTER(strata_moe_routing), _P, _I, _I64, _P, _I, _I, _I, _P,
+                                _P, _P],
+    "strata_moe_set_routing": [_P, C.POINTER(strata_moe_routing), _P],
+    "strata_moe_add_rmsnorm": [_P, _P, _P, _I, C.c_float, _I, _I, _P, _P, _I, _I, _P, _I64, _P,
+                               _I64, _P],
+    "strata_moe_dequant_rows": [_P, _I, _I64, _P, _I64, _I, _P, _I, _I, _I, _P, _P],
 }
 for _name, _args in _sig.items():
     _f = getattr(_lib, _name)
@@ -212,7 +229,46 @@ def strata_moe_route_noalloc(x, T, H, router_w, router_b, E, k, idx, w, offsets=
                                          stream))
 
 
+def strata_moe_route_logits(rule, logits, logits_type, ld, select_bias, T, E, k, idx, w,
+                            stream=None) -> None:
+    _check(_lib.strata_moe_route_logits(rule, logits, logits_type, ld, select_bias, T, E, k, idx,
+                                        w, stream))
+
+
+def strata_moe_set_routing(h, rule, select_bias=None) -> None:
+    """rule: strata_moe_routing or None; select_bias: float numpy [E] (host) or None."""
+    import numpy as np
+    keep = None if select_bias is None else np.ascontiguousarray(select_bias, dtype=np.float32)
+    _check(_lib.strata_moe_set_routing(h, rule, None if keep is None else keep.ctypes.data))
+
+
+def strata_moe_add_rmsnorm(x, delta, weight, weight_type, eps, T, H, h_out, xn, q8=0, group=0,
+                           q=None, q_stride=0, scale=None, scale_stride=0, stream=None) -> None:
+    _check(_lib.strata_moe_add_rmsnorm(x, delta, weight, weight_type, eps, T, H, h_out, xn, q8,
+                                       group, q, q_stride, scale, scale_stride, stream))
+
+
+def strata_moe_dequant_rows(q, q8, q_stride, scale, scale_stride, group, rows, n, n_src, H, out,
+                            stream=None) -> None:
+    _check(_lib.strata_moe_dequant_rows(q, q8, q_stride, scale, scale_stride, group, rows, n,
+                                        n_src, H, out, stream))
+
+
 # ----------------------------------------------------------------- convenience
+def make_routing(score="softmax", n_groups=1, top_groups=None, group_score="best", renorm=True,
+                 scale=1.0) -> strata_moe_routing:
+    """A routing rule: score "softmax" or "sigmoid"; n_groups runs of experts of
+    which top_groups (default: all) stay, by their "best" value or the sum of
+    their best two ("sum2"); renorm divides the weights by their sum over the
+    picks; scale multiplies them."""
+    scores = {"softmax": STRATA_SCORE_SOFTMAX, "sigmoid": STRATA_SCORE_SIGMOID}
+    groups = {"best": STRATA_GROUP_BEST, "sum2": STRATA_GROUP_SUM2}
+    if score not in scores or group_score not in groups:
+        raise ValueError(f"unknown score {score!r} or group_score {group_score!r}")
+    return strata_moe_routing(scores[score], n_groups, n_groups if top_groups is None else top_groups,
+                              groups[group_score], 1 if renorm else 0, scale)
+
+
 def make_config(shape, max_tokens: int) -> strata_moe_config:
     """Config from any object with hidden/n_experts/top_k/inter/bits/router_bias."""
     return strata_moe_config(shape.hidden, shape.n_experts, shape.top_k, shape.inter, shape.bits,
@@ -263,6 +319,10 @@ class Layer:
 
     def set_option(self, option, value):
         strata_moe_set_option(self.handle, option, value)
+
+    def set_routing(self, rule=None, select_bias=None):
+        """Pick and weigh by `rule` (make_routing) from now on; None: the default."""
+        strata_moe_set_routing(self.handle, rule, select_bias)
 
     def forward(self, x, out=None, stream=None):
         import torch

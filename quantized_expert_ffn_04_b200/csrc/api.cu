@@ -160,6 +160,11 @@ struct strata_moe {
     int path = 0;
     long long budget = kDefaultBudget;
     int decode_max_t = 64;
+    // routing rule (strata_moe_set_routing); without one, softmax top-k with
+    // renormalised weights
+    bool has_rule = false;
+    SelectPlan rule{};
+    float *select_bias = nullptr;  // [E], allocated by the first rule with a bias
 };
 
 namespace {
@@ -254,6 +259,7 @@ void free_handle(strata_moe *h) {
     dev_free(h->router_wp);
     dev_free(h->router_b);
     dev_free(h->router_split);
+    dev_free(h->select_bias);
     dev_free(h->ws);
     pinned_free(h->err_host);
     delete h;
@@ -313,6 +319,21 @@ __half *x16_of(strata_moe_t h, int T) {
 // the candidates.
 strata_status run_route(strata_moe_t h, const void *x, int T, int tile, cudaStream_t s) {
     const Geometry &g = h->geo;
+    if (h->has_rule) {
+        // a routing rule reads every expert's exact logit, at any T
+        probe(h, kStRouter, true, s);
+        launch_router(x, T, g.H, h->router_wp, h->router_b, g.E, h->logits, s);
+        probe(h, kStRouter, false, s);
+        const int stage = T > kSmallMaxT ? kStDispatch : kStTopk;
+        probe(h, stage, true, s);
+        cudaError_t ce = launch_route_logits(h->rule, h->logits, false, g.E, T, h->idx, h->wts, s);
+        if (ce != cudaSuccess)
+            return fail(STRATA_ERR_CUDA, "routing rule: %s", cudaGetErrorString(ce));
+        launch_dispatch(h->idx, T, g.k, g.E, h->cnt, h->off, h->list, h->slot, h->ds, h->units,
+                        h->n_units, tile, s, h->err);
+        probe(h, stage, false, s);
+        return check_launch("routing kernels");
+    }
     probe(h, kStRouter, true, s);
     if (T > kSmallMaxT) {
         launch_to_half(x, x16_of(h, T), (size_t)T * g.H, s);
@@ -351,7 +372,7 @@ bool use_decode_path(strata_moe_t h, int T) {
 // batch it supports.
 bool use_fused_path(strata_moe_t h, int T) {
     if (h->path == 3) return true;
-    return h->path == 0 && T <= h->decode_max_t && fused_decode_supported(h->geo, T);
+    return h->path == 0 && !h->has_rule && T <= h->decode_max_t && fused_decode_supported(h->geo, T);
 }
 
 // The whole layer in one launch (router, top-k, dispatch, experts, combine).
@@ -360,6 +381,8 @@ strata_status run_forward_fused(strata_moe_t h, const void *x, int T, void *y, b
     const Geometry &g = h->geo;
     if (!fused_decode_supported(g, T))
         return fail(STRATA_ERR_INVALID_ARG, "the fused decode kernel does not support T=%d", T);
+    if (h->has_rule)
+        return fail(STRATA_ERR_INVALID_ARG, "the fused decode kernel does not take a routing rule");
     ExpertWeights w{h->wq, h->wq + (size_t)g.E * g.expert_bytes};
     FusedArgs fa{};
     fa.x = x;
@@ -467,6 +490,8 @@ int strata_moe_launch_count(strata_moe_t h, int T) {
     // gather), and the combine.
     if (use_fused_path(h, T)) return 1;  // the fused layer kernel
     const bool decode = use_decode_path(h, T);
+    // with a routing rule: router, rule, 3 dispatch kernels, at any T
+    if (h->has_rule) return 5 + 1 + (decode ? 2 : 3) + 1;
     if (T <= kSmallMaxT) return 2 + 1 + (decode ? 2 : 3) + 1;
     return 6 + 1 + 3 + 1;
 }
@@ -659,6 +684,34 @@ strata_status strata_moe_set_option(strata_moe_t h, int option, int64_t value) {
     }
 }
 
+strata_status strata_moe_set_routing(strata_moe_t h, const strata_moe_routing *rule,
+                                     const float *select_bias) {
+    if (!h) return fail(STRATA_ERR_INVALID_ARG, "handle is NULL");
+    if (!rule && select_bias)
+        return fail(STRATA_ERR_INVALID_ARG, "a selection bias needs a routing rule");
+    SelectPlan plan{};
+    if (rule) {
+        const strata_status st =
+            make_select_plan(rule, h->geo.E, h->geo.k, "strata_moe_set_routing", &plan);
+        if (st != STRATA_OK) return st;
+    }
+    DeviceGuard guard(h->device);
+    if (!guard.ok) return fail(STRATA_ERR_CUDA, "cudaSetDevice(%d) failed", h->device);
+    cudaError_t ce = cudaDeviceSynchronize();  // calls in flight read the bias
+    if (ce != cudaSuccess) return cuda_fail(ce, "device synchronize");
+    if (select_bias) {
+        const size_t bytes = (size_t)h->geo.E * 4;
+        if (!h->select_bias && dev_malloc(&h->select_bias, bytes) != cudaSuccess)
+            return fail(STRATA_ERR_OOM, "selection bias allocation failed");
+        ce = cudaMemcpy(h->select_bias, select_bias, bytes, cudaMemcpyHostToDevice);
+        if (ce != cudaSuccess) return cuda_fail(ce, "selection bias upload");
+        plan.bias = h->select_bias;
+    }
+    h->rule = plan;
+    h->has_rule = rule != nullptr;
+    return STRATA_OK;
+}
+
 strata_status strata_moe_route(strata_moe_t h, const void *x_dev, int T, int32_t *idx_dev,
                                float *w_dev, int32_t *offsets_dev, int32_t *list_dev,
                                void *stream) {
@@ -789,6 +842,8 @@ strata_status strata_moe_stack_forward(const strata_moe_t *layers, int n_layers,
         view.screen_wmax = L->screen_wmax;
         view.screen_bmax = L->screen_bmax;
         view.cfg.has_router_bias = L->cfg.has_router_bias;
+        view.has_rule = L->has_rule;
+        view.rule = L->rule;
         st = run_forward(&view, l0->xn, T, h_dev, true, s);
         if (st != STRATA_OK) return st;
     }

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/strata_moe.h"
+
 namespace strata {
 
 // Geometry of one layer on the GPU.
@@ -83,6 +85,25 @@ void launch_screen_topk(const float *D, int R, const void *x, int T, int H, cons
 void launch_screen_debug(const float *D, int R, const void *x, int T, int H, const float *bias,
                          int E, float gam, float wmax, float bmax, float *a_out, float *eps_out,
                          cudaStream_t s);
+
+// ---- select.cu (routing rules)
+// A routing rule checked against a layer's or a call's sizes, with the lane
+// layout that follows from its groups (select.cuh).
+struct SelectPlan {
+    int E, k;
+    int score, renorm;            // STRATA_SCORE_*, 0/1
+    int n_groups, top_groups, gs; // gs = E / n_groups
+    int sum2;                     // groups by the sum of their best two
+    int log2_lanes;               // lanes of a warp that hold one group
+    float scale;
+    const float *bias;            // selection bias [E] (device) or null
+};
+// Fills `plan` (all but the bias); on a rule that does not fit, sets the error
+// message and returns the status.
+strata_status make_select_plan(const strata_moe_routing *rule, int E, int k, const char *who,
+                               SelectPlan *plan);
+cudaError_t launch_route_logits(const SelectPlan &plan, const void *logits, bool bf16,
+                                long long ld, int T, int32_t *idx, float *w, cudaStream_t s);
 
 // ---- gemv.cu (decode)
 struct ExpertWeights {
@@ -189,6 +210,29 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
+
+// The device that holds `p` becomes current for the scope of a call without a
+// handle; ok is false when p is not device memory.
+struct PointerDevice {
+    int prev = -1, dev = -1;
+    bool ok = false;
+    explicit PointerDevice(const void *p) {
+        cudaPointerAttributes a{};
+        if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+            cudaGetLastError();  // reported by the caller, not left sticky
+            return;
+        }
+        if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return;
+        dev = a.device;
+        if (cudaGetDevice(&prev) != cudaSuccess) return;
+        ok = prev == dev || cudaSetDevice(dev) == cudaSuccess;
+    }
+    ~PointerDevice() {
+        if (prev >= 0 && prev != dev) cudaSetDevice(prev);
+    }
+    PointerDevice(const PointerDevice &) = delete;
+    PointerDevice &operator=(const PointerDevice &) = delete;
+};
 
 // Set the thread-local message returned by strata_moe_last_error().
 void set_error_message(const char *msg);
