@@ -17,8 +17,9 @@ namespace strata {
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kInt8Max = 127.0f;
-// A group whose largest magnitude is below this stores zeros: its scale and
-// the reciprocal of it would leave fp32's normal range (448 / 2^-116 < 2^125).
+constexpr int kNormThreads = 1024;
+// A group whose largest magnitude is below this stores zeros: its scale would
+// leave fp32's normal range (2^-116 / 448 > 2^-125).
 constexpr float kTinyGroup = 1.2037062e-35f;  // 2^-116
 
 // ------------------------------------------------------------------ helpers
@@ -36,6 +37,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+}
+// bf16(f32(x) + f32(d)) of eight pairs.  One rounded bf16 addition gives the same:
+// fp32 rounds the sum only where d is below 2^-16 of x (or x of d), and there
+// both forms return the larger of the two.
+__device__ __forceinline__ uint4 add8(const uint4 &x, const uint4 &d) {
+    auto add = [](uint32_t p, uint32_t q) {
+        const __nv_bfloat162 v = __hadd2_rn(*reinterpret_cast<__nv_bfloat162 *>(&p), *reinterpret_cast<__nv_bfloat162 *>(&q));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    };
+    return make_uint4(add(x.x, d.x), add(x.y, d.y), add(x.z, d.z), add(x.w, d.w));
 }
 // Four values to four codes; the first in the lowest byte.
 template <int kQ8>
@@ -61,90 +72,141 @@ struct NormArgs {
     float *scale;
     long long q_stride, scale_stride;
     float eps, inv_h;
-    int T, H, group, weight_f32;
+    int T, H, weight_f32;
 };
 
-// Reduce over the block's kThreads threads; every thread gets the result.
-template <int kThreads, typename V, typename F>
-__device__ __forceinline__ V block_reduce(V v, V *scratch, F op) {
+// Largest of two magnitudes; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+// Sum over the row's 32-vector blocks: v[i] is this thread's part of block
+// i * warps + warp.  A tree inside each block, then one over the blocks, so the
+// sum does not depend on how many vectors a thread holds.
+template <int NV, typename V>
+__device__ __forceinline__ V row_sum(V (&v)[NV], V *scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (kThreads == 32) return v;
-    const int warp = threadIdx.x >> 5;
-    __syncthreads();  // the scratch's previous use
-    if ((threadIdx.x & 31) == 0) scratch[warp] = v;
+    for (int i = 0; i < NV; i++) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (lane == 0) scratch[i * warps + warp] = v[i];
+    }
     __syncthreads();
-    v = scratch[0];
+    const int blocks = NV * warps;
+    V sum = lane < blocks ? scratch[lane] : (V)0;
+    if (NV > 1) sum += lane + 32 < blocks ? scratch[lane + 32] : (V)0;
 #pragma unroll
-    for (int i = 1; i < kThreads / 32; i++) v = op(v, scratch[i]);
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+__device__ __forceinline__ float row_max(float v, float *scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if (lane == 0) scratch[warp] = v;
+    __syncthreads();
+    v = scratch[lane < warps ? lane : 0];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
-// One block per row; thread i holds the 16-byte vectors i, i + kThreads, ...
-template <int kThreads, int NV, int kQ8, bool kF32Weight>
-__global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float fs[kThreads / 32];
-    __shared__ uint32_t us[kThreads / 32];
-    __shared__ double ds[kThreads / 32];
+// One row a block; thread i holds the 16-byte vectors i and (NV == 2)
+// i + blockDim.x.  kGroup: columns a scale covers, 0 for the whole row, -1 for
+// no 8-bit output.
+template <int NV, int kQ8, int kGroup, bool kF32Weight>
+__global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float fs[64], ms[32];
+    __shared__ double ds[64];
     grid_launch_dependents();
     grid_dependency_wait();
-    const int nv = a.H >> 3, tid = threadIdx.x;
-    const long long row = (long long)blockIdx.x * nv;
+    const int nv = a.H >> 3, tid = threadIdx.x, threads = blockDim.x;
+    const long long t = blockIdx.x, row = t * nv;
     uint4 hv[NV], dv[NV];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int c = i * kThreads + tid;
+        const int c = i * threads + tid;
         hv[i] = c < nv ? a.x[row + c] : make_uint4(0, 0, 0, 0);
-        dv[i] = a.delta && c < nv ? a.delta[row + c] : make_uint4(0, 0, 0, 0);
+        if (a.delta) dv[i] = c < nv ? a.delta[row + c] : make_uint4(0, 0, 0, 0);
     }
-    float ss = 0.0f;
+    float h[NV][8], part[NV];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const int c = i * kThreads + tid;
-        float f[8], d[8];
-        unpack8(hv[i], f);
-        if (a.delta) {
-            unpack8(dv[i], d);
-#pragma unroll
-            for (int q = 0; q < 8; q++) f[q] = __fadd_rn(f[q], d[q]);
-            hv[i] = pack8(f);
-            unpack8(hv[i], f);
-        }
+        const int c = i * threads + tid;
+        if (a.delta) hv[i] = add8(hv[i], dv[i]);
         if (a.h_out && c < nv) a.h_out[row + c] = hv[i];
+        unpack8(hv[i], h[i]);
+        part[i] = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 8; q++) ss = fmaf(f[q], f[q], ss);
+        for (int q = 0; q < 8; q++) part[i] = fmaf(h[i][q], h[i][q], part[i]);
     }
-    auto add = [](float p, float q) { return p + q; };
-    auto umax = [](uint32_t p, uint32_t q) { return p > q ? p : q; };
-    ss = block_reduce<kThreads>(ss, fs, add);
-    // r = 1 / sqrt(mean + eps) as unit * rr: 64 bits where the squares' sum
-    // leaves fp32's range (unit a power of two, so that both are normal floats)
-    float unit = 1.0f, rr;
-    if ((ss < 1e-30f && a.eps < 1e-30f) || !(ss < 1e37f)) {
-        double sd = 0.0;
+    const float ss = row_sum<NV>(part, fs);
+    // r = 1 / sqrt(mean + eps).  Where the squares' sum comes near the ends of
+    // fp32's range: in 64 bits, and r = unit * rr with unit a power of two that
+    // h is multiplied by first
+    float r = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(ss, a.inv_h, a.eps)));
+    if ((ss < 0x1p-60f && a.eps < 0x1p-60f) || !(ss < 0x1p60f)) {
+        double dp[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            float f[8];
-            unpack8(hv[i], f);
+            dp[i] = 0.0;
 #pragma unroll
-            for (int q = 0; q < 8; q++) sd = fma((double)f[q], (double)f[q], sd);
+            for (int q = 0; q < 8; q++) dp[i] = fma((double)h[i][q], (double)h[i][q], dp[i]);
         }
-        sd = block_reduce<kThreads>(sd, ds, [](double p, double q) { return p + q; });
-        const double r = 1.0 / sqrt(sd / a.H + (double)a.eps);
-        const int ex = r > 0.0 && r < INFINITY ? max(-126, min(126, ilogb(r))) : 0;
-        unit = __uint_as_float((uint32_t)(127 + ex) << 23);
-        rr = (float)(r / (double)unit);
-    } else {
-        rr = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(ss, a.inv_h, a.eps)));
-    }
-    uint32_t row_max = 0;
-    float inv = 0.0f;
-    auto values = [&](int i, float (&y)[8]) {  // y of vector i
-        const int c = i * kThreads + tid;
-        float w[8];
+        const double rd = 1.0 / sqrt(row_sum<NV>(dp, ds) / a.H + (double)a.eps);
+        const int ex = rd > 0.0 && rd < INFINITY ? max(-126, min(126, ilogb(rd))) : 0;
+        const float unit = __uint_as_float((uint32_t)(127 + ex) << 23);
+        r = (float)(rd / (double)unit);
 #pragma unroll
-        for (int q = 0; q < 8; q++) w[q] = 1.0f;
+        for (int i = 0; i < NV; i++)
+#pragma unroll
+            for (int q = 0; q < 8; q++) h[i][q] *= unit;
+    }
+    constexpr float kMax = kQ8 == STRATA_Q8_E4M3 ? kE4m3Max : kInt8Max;
+    // y = t r with t = h w (exact for bf16 weights).  A code is the rounded
+    // quotient kMax t / max|t|: (c t) / m with m = max|t| scaled into [1, 2) and c
+    // = kMax times the same power of two, both exact where t is.  The quotient is
+    // corrected once by its remainder (Markstein's method), which makes it exact
+    // where it is representable: a value exactly between two codes goes to the
+    // even one, as it does in 64 bits.
+    struct Group {
+        float c, m, inv;
+    };
+    auto group_of = [&](float mt, float &scale) {
+        const float y = mt * r;
+        Group g{0.0f, 1.0f, 1.0f};
+        scale = y * (1.0f / kMax);
+        if (y >= kTinyGroup && y < INFINITY) {
+            const uint32_t bits = __float_as_uint(mt);
+            g.m = __uint_as_float((bits & 0x007fffffu) | 0x3f800000u);
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.inv) : "f"(g.m));
+            g.c = __uint_as_float(__float_as_uint(kMax) + ((127u - (bits >> 23)) << 23));
+        } else {
+            scale = y < INFINITY ? 0.0f : __uint_as_float(0x7fc00000u);
+        }
+        return g;
+    };
+    auto emit = [&](int i, const Group &g) {
+        const int c = i * threads + tid;
+        float k[8];
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            const float n = h[i][q] * g.c, q0 = n * g.inv;
+            k[q] = fmaf(fmaf(-g.m, q0, n), g.inv, q0);
+        }
+        uint2 o = make_uint2(codes4<kQ8>(k[0], k[1], k[2], k[3]), codes4<kQ8>(k[4], k[5], k[6], k[7]));
+        if (g.c == 0.0f) o = make_uint2(0, 0);  // also where a value is not finite
+        if (c < nv) *reinterpret_cast<uint2 *>(a.q + t * a.q_stride + 8 * c) = o;
+    };
+    float largest = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const int c = i * threads + tid;
         if (a.weight && c < nv) {
+            float w[8];
             if (kF32Weight) {
                 const float4 u = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * c);
                 const float4 v = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * c + 1);
@@ -152,86 +214,64 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(const __grid_cons
             } else {
                 unpack8(__ldg(reinterpret_cast<const uint4 *>(a.weight) + c), w);
             }
+#pragma unroll
+            for (int q = 0; q < 8; q++) h[i][q] *= w[q];
         }
-        unpack8(hv[i], y);
+        if (a.xn && c < nv) {
+            float o[8];
 #pragma unroll
-        for (int q = 0; q < 8; q++) y[q] = (y[q] * unit) * rr * w[q];
-    };
-    auto emit = [&](int i, const float (&y)[8], float mul) {
-        const int c = i * kThreads + tid;
-        if (c >= nv) return;
-        uint2 o;
-        o.x = codes4<kQ8>(y[0] * mul, y[1] * mul, y[2] * mul, y[3] * mul);
-        o.y = codes4<kQ8>(y[4] * mul, y[5] * mul, y[6] * mul, y[7] * mul);
-        if (mul == 0.0f) o = make_uint2(0, 0);  // also where a value is not finite
-        *reinterpret_cast<uint2 *>(a.q + (long long)blockIdx.x * a.q_stride + 8 * c) = o;
-    };
-    constexpr float kMax = kQ8 == STRATA_Q8_E4M3 ? kE4m3Max : kInt8Max;
-    // group maximum (float bits; a NaN is above all) -> stored scale and multiplier
-    auto scale_of = [&](uint32_t bits, float &mul) {
-        const float m = __uint_as_float(bits);
-        if (bits >= 0x7f800000u) {
-            mul = 0.0f;
-            return __uint_as_float(0x7fc00000u);
+            for (int q = 0; q < 8; q++) o[q] = h[i][q] * r;
+            a.xn[row + c] = pack8(o);
         }
-        mul = m < kTinyGroup ? 0.0f : __fdiv_rn(kMax, m);
-        return m < kTinyGroup ? 0.0f : __fdiv_rn(m, kMax);
-    };
-    float *srow = a.q ? a.scale + (long long)blockIdx.x * a.scale_stride : nullptr;
+        if (kGroup < 0) continue;
+        float m = fabsf(h[i][0]);
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const int c = i * kThreads + tid;
-        float y[8];
-        values(i, y);
-        if (a.xn && c < nv) a.xn[row + c] = pack8(y);
-        if (!a.q) continue;
-        uint32_t am = 0;
+        for (int q = 1; q < 8; q++) m = max_nan(m, fabsf(h[i][q]));
+        if (kGroup > 0) {
+            // kGroup / 8 neighbouring threads hold a group
 #pragma unroll
-        for (int q = 0; q < 8; q++) am = umax(am, __float_as_uint(y[q]) & 0x7fffffffu);
-        if (a.group) {
-            // group / 8 neighbouring threads hold a group
-            for (int o = a.group >> 4; o >= 1; o >>= 1) am = umax(am, __shfl_xor_sync(0xffffffffu, am, o));
-            float mul;
-            const float sc = scale_of(am, mul);
-            if (c < nv && 8 * c % a.group == 0) srow[8 * c / a.group] = sc;
-            emit(i, y, mul);
+            for (int o = kGroup / 16; o >= 1; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float scale;
+            const Group g = group_of(m, scale);
+            constexpr int kVecs = kGroup > 0 ? kGroup / 8 : 1;
+            if (c < nv && c % kVecs == 0) a.scale[t * a.scale_stride + c / kVecs] = scale;
+            emit(i, g);
         } else {
-            row_max = umax(row_max, c < nv ? am : 0u);
+            largest = max_nan(largest, m);  // a vector past the row holds zeros
         }
     }
-    if (a.q && !a.group) {
-        row_max = block_reduce<kThreads>(row_max, us, umax);
-        const float sc = scale_of(row_max, inv);
-        if (tid == 0) srow[0] = sc;
+    if (kGroup == 0) {
+        float scale;
+        const Group g = group_of(row_max(largest, ms), scale);
+        if (tid == 0) a.scale[t * a.scale_stride] = scale;
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            float y[8];
-            values(i, y);
-            emit(i, y, inv);
-        }
+        for (int i = 0; i < NV; i++) emit(i, g);
     }
 }
 
-template <int NV, int kQ8, bool kF32Weight>
+template <int kQ8, int kGroup, bool kF32Weight>
 static cudaError_t run_norm(const NormArgs &a, cudaStream_t s) {
-    return launch_pdl(add_rmsnorm_kernel<128, NV, kQ8, kF32Weight>, dim3(a.T), dim3(128), 0, s, a);
+    const int nv = a.H / 8;
+    // One vector a thread while a row finds an SM of its own (148 of them): the
+    // row's latency is all that counts.  Two above, so that more rows are in
+    // flight and the block's reduction is shared by more work.
+    if (a.T <= 148 && nv <= kNormThreads)
+        return launch_pdl(add_rmsnorm_kernel<1, kQ8, kGroup, kF32Weight>, dim3(a.T), dim3((nv + 31) / 32 * 32), 0, s, a);
+    return launch_pdl(add_rmsnorm_kernel<2, kQ8, kGroup, kF32Weight>, dim3(a.T), dim3((nv / 2 + 31) / 32 * 32), 0, s, a);
 }
-template <int kQ8, bool kF32Weight>
-static cudaError_t run_norm_nv(const NormArgs &a, cudaStream_t s) {
-    const int nv = (a.H / 8 + 127) / 128;
-    if (nv <= 1) return run_norm<1, kQ8, kF32Weight>(a, s);
-    if (nv <= 2) return run_norm<2, kQ8, kF32Weight>(a, s);
-    if (nv <= 3) return run_norm<3, kQ8, kF32Weight>(a, s);
-    if (nv <= 4) return run_norm<4, kQ8, kF32Weight>(a, s);
-    if (nv <= 6) return run_norm<6, kQ8, kF32Weight>(a, s);
-    if (nv <= 8) return run_norm<8, kQ8, kF32Weight>(a, s);
-    return run_norm<16, kQ8, kF32Weight>(a, s);
+template <int kQ8>
+static cudaError_t run_norm_group(const NormArgs &a, int group, cudaStream_t s) {
+    switch (group) {
+    case 0: return a.weight_f32 ? run_norm<kQ8, 0, true>(a, s) : run_norm<kQ8, 0, false>(a, s);
+    case 32: return a.weight_f32 ? run_norm<kQ8, 32, true>(a, s) : run_norm<kQ8, 32, false>(a, s);
+    case 64: return a.weight_f32 ? run_norm<kQ8, 64, true>(a, s) : run_norm<kQ8, 64, false>(a, s);
+    default: return a.weight_f32 ? run_norm<kQ8, 128, true>(a, s) : run_norm<kQ8, 128, false>(a, s);
+    }
 }
 
-static cudaError_t launch_add_rmsnorm(const NormArgs &a, int q8, cudaStream_t s) {
-    if (q8 == STRATA_Q8_INT8)
-        return a.weight_f32 ? run_norm_nv<STRATA_Q8_INT8, true>(a, s) : run_norm_nv<STRATA_Q8_INT8, false>(a, s);
-    return a.weight_f32 ? run_norm_nv<STRATA_Q8_E4M3, true>(a, s) : run_norm_nv<STRATA_Q8_E4M3, false>(a, s);
+static cudaError_t launch_add_rmsnorm(const NormArgs &a, int q8, int group, cudaStream_t s) {
+    if (!a.q) return a.weight_f32 ? run_norm<STRATA_Q8_E4M3, -1, true>(a, s) : run_norm<STRATA_Q8_E4M3, -1, false>(a, s);
+    return q8 == STRATA_Q8_INT8 ? run_norm_group<STRATA_Q8_INT8>(a, group, s) : run_norm_group<STRATA_Q8_E4M3>(a, group, s);
 }
 
 // ------------------------------------------------------------------ read back
@@ -241,7 +281,7 @@ struct DequantArgs {
     const int32_t *rows;
     uint4 *out;
     long long q_stride, scale_stride;
-    int group, n, n_src, H;
+    int log2_group, n, n_src, H;  // log2_group 31: one scale a row
 };
 
 // Four codes as floats.
@@ -263,43 +303,48 @@ __device__ __forceinline__ void values4(uint32_t u, float (&f)[4]) {
     }
 }
 
-// One warp per row; a lane turns 16 codes into 32 bytes.
+// One warp per row, a lane turns 8 codes (one load) into 16 bytes (one store),
+// kAhead loads before the first store.
+constexpr int kDequantWarps = 4, kAhead = 10;
 template <int kQ8>
-__global__ __launch_bounds__(128) void dequant_rows_kernel(const __grid_constant__ DequantArgs a) {
+__global__ __launch_bounds__(32 * kDequantWarps) void dequant_rows_kernel(const __grid_constant__ DequantArgs a) {
     grid_launch_dependents();
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * 4 + (threadIdx.x >> 5);
+    const long long i = (long long)blockIdx.x * kDequantWarps + (threadIdx.x >> 5);
     if (i >= a.n) return;
-    const int r = a.rows ? a.rows[i] : i;
+    const int r = a.rows ? a.rows[i] : (int)i;
     if ((unsigned)r >= (unsigned)a.n_src) return;
-    const uint8_t *q = a.q + (long long)r * a.q_stride;
+    const int nv = a.H >> 3;
+    const uint2 *q = reinterpret_cast<const uint2 *>(a.q + (long long)r * a.q_stride);
     const float *sc = a.scale + (long long)r * a.scale_stride;
-    uint4 *o = a.out + (long long)i * (a.H >> 3);
-    for (int c = lane; c < (a.H >> 4); c += 32) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(q + 16 * c);
-        const float s = sc[a.group ? 16 * c / a.group : 0];
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float f[16];
+    uint4 *o = a.out + i * nv;
+    for (int c0 = lane; c0 < nv; c0 += 32 * kAhead) {
+        uint2 u[kAhead];
+        float s[kAhead];
 #pragma unroll
-        for (int k = 0; k < 4; k++) {
-            float g[4];
-            values4<kQ8>(w[k], g);
-#pragma unroll
-            for (int j = 0; j < 4; j++) f[4 * k + j] = g[j] * s;
+        for (int k = 0; k < kAhead; k++) {
+            const int c = c0 + 32 * k;
+            u[k] = c < nv ? q[c] : make_uint2(0, 0);
+            s[k] = c < nv ? sc[(8 * c) >> a.log2_group] : 0.0f;
         }
-        float lo[8], hi[8];
 #pragma unroll
-        for (int k = 0; k < 8; k++) lo[k] = f[k], hi[k] = f[8 + k];
-        o[2 * c] = pack8(lo);
-        o[2 * c + 1] = pack8(hi);
+        for (int k = 0; k < kAhead; k++) {
+            const int c = c0 + 32 * k;
+            float lo[4], hi[4];
+            values4<kQ8>(u[k].x, lo);
+            values4<kQ8>(u[k].y, hi);
+            const float f[8] = {lo[0] * s[k], lo[1] * s[k], lo[2] * s[k], lo[3] * s[k],
+                                hi[0] * s[k], hi[1] * s[k], hi[2] * s[k], hi[3] * s[k]};
+            if (c < nv) __stcs(o + c, pack8(f));
+        }
     }
 }
 
 static cudaError_t launch_dequant_rows(const DequantArgs &a, int q8, cudaStream_t s) {
-    const dim3 grid((unsigned)((a.n + 3) / 4));
+    const dim3 grid((unsigned)(((long long)a.n + kDequantWarps - 1) / kDequantWarps));
     return launch_pdl(q8 == STRATA_Q8_INT8 ? dequant_rows_kernel<STRATA_Q8_INT8> : dequant_rows_kernel<STRATA_Q8_E4M3>,
-                      grid, dim3(128), 0, s, a);
+                      grid, dim3(32 * kDequantWarps), 0, s, a);
 }
 
 // A call's refusal: message and status.
@@ -397,9 +442,8 @@ strata_status strata_moe_add_rmsnorm(const void *x_dev, const void *delta_dev,
     a.inv_h = 1.0f / (float)H;
     a.T = T;
     a.H = H;
-    a.group = q_dev ? group : 0;
     a.weight_f32 = weight_type == STRATA_F32;
-    return launched(who, launch_add_rmsnorm(a, q_dev ? q8 : STRATA_Q8_E4M3, (cudaStream_t)stream));
+    return launched(who, launch_add_rmsnorm(a, q8, group, (cudaStream_t)stream));
 }
 
 strata_status strata_moe_dequant_rows(const void *q_dev, int q8, int64_t q_stride,
@@ -433,7 +477,7 @@ strata_status strata_moe_dequant_rows(const void *q_dev, int q8, int64_t q_strid
     a.out = (uint4 *)out_dev;
     a.q_stride = q_stride;
     a.scale_stride = scale_stride;
-    a.group = group;
+    a.log2_group = group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : 31;
     a.n = n;
     a.n_src = n_src;
     a.H = H;

@@ -11,7 +11,7 @@ subnormal; int8 by half a scale.
 import numpy as np
 import pytest
 
-from tests.front_ref import norm_rows
+from tests.front_ref import norm_rows, round_to
 
 pytestmark = pytest.mark.gpu
 
@@ -143,6 +143,52 @@ def test_norm_options():
     n.go()
     torch.cuda.synchronize()
     assert torch.equal(n.h[:T], x)
+
+
+def test_the_residual_sum_is_the_fp32_sum_rounded_once():
+    """bf16(f32(x) + f32(delta)) bit for bit over all exponents, subnormal values
+    and overflow to infinity included."""
+    T, H = 64, 4096
+    rng = np.random.default_rng(5)
+    bits = rng.integers(0, 1 << 16, (2, T, H)).astype(np.uint16)
+    near = rng.integers(-1200, 1200, (T // 2, H))  # delta's exponent near x's, and nine below it
+    bits[1, :T // 2] = np.clip(bits[0, :T // 2].astype(np.int64) + near, 0, 0xFFFF)
+    x, d = (torch.from_numpy(b.view(np.int16).copy()).view(torch.bfloat16).cuda() for b in bits)
+    x, d = (torch.where(torch.isfinite(t), t, torch.ones_like(t)) for t in (x, d))
+    n = Norm(x, d, xn=False)
+    n.go()
+    torch.cuda.synchronize()
+    assert torch.equal(n.h[:T].view(torch.int16), (x.float() + d.float()).to(torch.bfloat16).view(torch.int16))
+
+
+def test_rows_do_not_depend_on_their_batch():
+    """The same row alone, in a small and in a large batch: the same bits."""
+    H = 2592
+    x, d, w = inputs(400, H, 6, torch.float32)
+    outs = []
+    for T in (400, 148, 1):
+        n = Norm(x[:T], d[:T], w, q8="e4m3", group=32)
+        n.go()
+        torch.cuda.synchronize()
+        outs.append((n.xn[0].clone(), n.q[0].clone(), n.scale[0].clone()))
+    for o in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+def test_codes_of_bf16_weights_are_the_64_bit_ones():
+    """Every code as 64-bit arithmetic gives it, exact halves going to the even one."""
+    for q8, group in (("e4m3", 128), ("e4m3", 0), ("int8", 64)):
+        x, d, w = inputs(200, 1024, 17, torch.bfloat16)
+        x[:, ::3] = x[:, :1] * 0.25  # many equal values and exact ratios
+        n = Norm(x, d, w, q8=q8, group=group)
+        n.go()
+        torch.cuda.synchronize()
+        h, _ = norm_rows(f64(x), f64(d), None, 1e-6)
+        t = (h * f64(w)).reshape(200, n.ns, -1)
+        # the product is exact, so the one rounded quotient is a half only where the exact one is
+        a = t * Q8[q8][2] / np.abs(t).max(2, keepdims=True)
+        want = round_to(a, 8, -6) if q8 == "e4m3" else np.round(a)
+        assert np.array_equal(n.codes()[0], want.reshape(200, -1))
 
 
 @pytest.mark.parametrize("eps", [0.0, 1e-35, 1e-6, 1.0])
