@@ -87,14 +87,13 @@ void launch_screen_debug(const float *D, int R, const void *x, int T, int H, con
                          cudaStream_t s);
 
 // ---- select.cu (routing rules)
-// A routing rule checked against a layer's or a call's sizes, with the lane
-// layout that follows from its groups (select.cuh).
+// A routing rule checked against a layer's or a call's sizes.
 struct SelectPlan {
     int E, k;
     int score, renorm;            // STRATA_SCORE_*, 0/1
     int n_groups, top_groups, gs; // gs = E / n_groups
     int sum2;                     // groups by the sum of their best two
-    int log2_lanes;               // lanes of a warp that hold one group
+    int log2_groups;              // of n_groups rounded up to a power of two
     float scale;
     const float *bias;            // selection bias [E] (device) or null
 };
@@ -104,6 +103,12 @@ strata_status make_select_plan(const strata_moe_routing *rule, int E, int k, con
                                SelectPlan *plan);
 cudaError_t launch_route_logits(const SelectPlan &plan, const void *logits, bool bf16,
                                 long long ld, int T, int32_t *idx, float *w, cudaStream_t s);
+// ---- select_batch.cu: the same for many tokens, where route_batch_lanes (lanes
+// of a warp that take one token) is below 32; vec: rows and bias are read in
+// aligned fours
+int route_batch_lanes(const SelectPlan &plan, int T);
+cudaError_t launch_route_batch(const SelectPlan &plan, const void *logits, bool bf16, long long ld,
+                               int T, int32_t *idx, float *w, bool vec, cudaStream_t s);
 
 // ---- gemv.cu (decode)
 struct ExpertWeights {

@@ -1,8 +1,11 @@
 // Routing rules: picks and weights from logits (strata_moe_route_logits), and
 // the same kernel for a layer whose rule is set (strata_moe_set_routing).
 //
-// One warp per token (select.cuh).  The work is one read of the logits and a
-// few hundred instructions a token.
+// One warp per token here, several tokens a warp in select_batch.cu (select.cuh).
+// The work is one read of the logits and a few hundred instructions a token; the
+// instructions bound it: 65536 tokens of 256 experts (8 groups, sigmoid scores
+// with a bias) take 39 us, 479 instructions a token at 66 % of the issue slots,
+// where the read alone would take 11; without groups and bias 23 us.
 #include <math.h>
 #include <stdio.h>
 
@@ -12,88 +15,19 @@
 
 namespace strata {
 
-constexpr int kSelectWarps = 4;
-
-// Four logits (or biases) of a lane: experts j .. j + 3 of a group of gs, e0
-// the group's first.  Entries past the group are -inf.
-template <bool kVec>
-__device__ __forceinline__ void load_four(LogitRow row, int e0, int j, int gs, float (&out)[4]) {
-    float f[4];
-    if (kVec) {  // gs a multiple of 4 and the row aligned: all four or none
-        const int e = e0 + (j < gs ? j : 0);
-        if (row.bf16) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(reinterpret_cast<const __nv_bfloat16 *>(row.p) + e);
-            f[0] = __uint_as_float(u.x << 16), f[1] = __uint_as_float(u.x & 0xffff0000u);
-            f[2] = __uint_as_float(u.y << 16), f[3] = __uint_as_float(u.y & 0xffff0000u);
-        } else {
-            const float4 u = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(row.p) + e);
-            f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; q++) out[q] = j < gs ? LogitRow::clean(f[q]) : -INFINITY;
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const float l = row.at(e0 + (j + q < gs ? j + q : 0));
-            out[q] = j + q < gs ? l : -INFINITY;
-        }
-    }
-}
-
-template <int NQ, bool kVec>
-__global__ __launch_bounds__(32 * kSelectWarps) void route_logits_kernel(
-    const __grid_constant__ SelectPlan p, const void *__restrict__ logits, int bf16, long long ld,
-    int T, int32_t *__restrict__ idx, float *__restrict__ w) {
-    __shared__ SelectSlot slots[kSelectWarps][32];
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kSelectWarps + warp;
-    if (t >= T) return;
-    const int L = 1 << p.log2_lanes, g = lane >> p.log2_lanes, r = lane & (L - 1);
-    const bool active = g < p.n_groups;
-    const int e0 = active ? g * p.gs : 0, gs = active ? p.gs : 0;
-    const LogitRow row{reinterpret_cast<const char *>(logits) + (long long)t * ld * (bf16 ? 2 : 4), bf16 != 0};
-    const LogitRow brow{p.bias, false};
-    float v[NQ], b[NQ];
-#pragma unroll
-    for (int i = 0; i < NQ; i += 4) {
-        float f[4];
-        const int j = i * L + 4 * r;
-        load_four<kVec>(row, e0, j, gs, f);
-#pragma unroll
-        for (int q = 0; q < 4; q++) v[i + q] = f[q];
-        if (p.bias) load_four<false>(brow, e0, j, gs, f);
-#pragma unroll
-        for (int q = 0; q < 4; q++) b[i + q] = p.bias ? f[q] : 0.0f;
-    }
-    int rank, e;
-    float wt;
-    select_token<NQ>(p, row, lane, v, b, slots[warp], rank, e, wt);
-    if (rank < p.k) {
-        idx[(long long)t * p.k + rank] = e;
-        w[(long long)t * p.k + rank] = wt;
-    }
-}
-
-template <int NQ>
-static cudaError_t run_route(const SelectPlan &p, const void *logits, bool bf16, long long ld, int T,
-                             int32_t *idx, float *w, bool vec, cudaStream_t s) {
-    const dim3 grid((T + kSelectWarps - 1) / kSelectWarps), block(32 * kSelectWarps);
-    return launch_pdl(vec ? route_logits_kernel<NQ, true> : route_logits_kernel<NQ, false>, grid,
-                      block, 0, s, p, logits, bf16 ? 1 : 0, ld, T, idx, w);
-}
-
 cudaError_t launch_route_logits(const SelectPlan &p, const void *logits, bool bf16, long long ld,
                                 int T, int32_t *idx, float *w, cudaStream_t s) {
-    // four logits a load where every group of every row starts at a multiple of it
-    const bool vec = p.gs % 4 == 0 && ld % 4 == 0 && ((uintptr_t)logits % (bf16 ? 8 : 16)) == 0;
-    const int L = 1 << p.log2_lanes, nq = 4 * ((p.gs + 4 * L - 1) / (4 * L));
-    if (nq <= 4) return run_route<4>(p, logits, bf16, ld, T, idx, w, vec, s);
-    if (nq <= 8) return run_route<8>(p, logits, bf16, ld, T, idx, w, vec, s);
-    if (nq <= 16) return run_route<16>(p, logits, bf16, ld, T, idx, w, vec, s);
-    if (nq <= 32) return run_route<32>(p, logits, bf16, ld, T, idx, w, vec, s);
-    return run_route<64>(p, logits, bf16, ld, T, idx, w, vec, s);  // 1024 / 17 = 60 experts a lane
+    // four logits a load where every group of every row (and the bias) starts at
+    // a multiple of it
+    const bool vec = p.gs % 4 == 0 && ld % 4 == 0 && ((uintptr_t)logits % (bf16 ? 8 : 16)) == 0 &&
+                     ((uintptr_t)p.bias % 16) == 0;
+    if (route_batch_lanes(p, T) < 32) return launch_route_batch(p, logits, bf16, ld, T, idx, w, vec, s);
+    const int n = lane_elements(p, 32);
+    if (n <= 4) return run_route<32, 4>(p, logits, bf16, ld, T, idx, w, vec, s);
+    if (n <= 8) return run_route<32, 8>(p, logits, bf16, ld, T, idx, w, vec, s);
+    if (n <= 16) return run_route<32, 16>(p, logits, bf16, ld, T, idx, w, vec, s);
+    if (n <= 32) return run_route<32, 32>(p, logits, bf16, ld, T, idx, w, vec, s);
+    return run_route<32, 64>(p, logits, bf16, ld, T, idx, w, vec, s);  // 1024 / 17 = 60 experts a lane
 }
 
 strata_status make_select_plan(const strata_moe_routing *rule, int E, int k, const char *who,
@@ -134,8 +68,7 @@ strata_status make_select_plan(const strata_moe_routing *rule, int E, int k, con
     p.top_groups = grouped ? rule->top_groups : 1;
     p.gs = E / p.n_groups;
     p.sum2 = grouped && rule->group_score == STRATA_GROUP_SUM2;
-    p.log2_lanes = 5;
-    while ((32 >> p.log2_lanes) < p.n_groups) p.log2_lanes--;
+    while ((1 << p.log2_groups) < p.n_groups) p.log2_groups++;
     p.scale = rule->scale;
     *plan = p;
     return STRATA_OK;

@@ -91,6 +91,40 @@ def test_odd_sizes(E, k, n, top):
             check(logits_of(19, E, E + k), k, bias, score=score, n_groups=n, top_groups=top, group_score=gs)
 
 
+@pytest.mark.parametrize("E,k,n,top", [(256, 8, 8, 4), (256, 10, 1, 1), (512, 10, 1, 1), (512, 16, 4, 2), (160, 6, 8, 3), (64, 16, 2, 1),
+                                       (16, 2, 1, 1), (1024, 16, 16, 1), (480, 15, 16, 3), (768, 4, 1, 1), (250, 7, 5, 2), (31, 16, 1, 1),
+                                       (1000, 12, 8, 8), (60, 1, 15, 1), (256, 16, 1, 1)])
+def test_large_batches(E, k, n, top):
+    """Batches large enough for several tokens a warp: every token against the
+    call of few, and a sample (with masked and equal rows) against the plain form."""
+    T = 17001 if k % 2 == 0 else 9001
+    rng = np.random.default_rng(E + k)
+    l = logits_of(T, E, E)
+    odd = rng.choice(T, 60, replace=False)
+    l[odd[:10], : E // 2] = -np.inf
+    l[odd[10:20]] = 0.25
+    l[odd[20:30], ::3] = np.nan
+    l[odd[30:40]] = -np.inf
+    l[odd[40:50]] = np.round(l[odd[40:50]])
+    l[odd[50:], rng.integers(0, E)] = np.inf
+    sample = np.concatenate([odd, [0, 1, 2, 3, 4, T - 5, T - 4, T - 3, T - 2, T - 1], rng.choice(T, 60)])
+    for dt in (torch.float32, torch.bfloat16):
+        t = torch.from_numpy(l).cuda().to(dt)
+        host = t.float().cpu().numpy()
+        for kw in [dict(score="sigmoid", scale=2.5), dict(score="softmax", renorm=False)]:
+            for bias in (None, bias_of(E, 3, 0.05 if kw["score"] == "sigmoid" else 0.2 / E)):
+                kw.update(n_groups=n, top_groups=top, group_score="sum2" if E // n >= 2 and bias is not None else "best")
+                idx, w = call(t, k, bias, **kw)
+                ridx, rw = route_rule(host[sample], k, bias=bias, **kw)
+                assert np.array_equal(idx[sample], ridx)
+                np.testing.assert_allclose(w[sample], rw, rtol=W_TOL if kw["score"] == "sigmoid" else W_TOL_PLAIN_SOFTMAX, atol=1e-37)
+                for t0 in range(0, T, 1000):
+                    part = t[t0:t0 + 1000].contiguous()
+                    i2, w2 = call(part, k, bias, **kw)
+                    assert np.array_equal(idx[t0:t0 + 1000], i2)
+                    np.testing.assert_allclose(w[t0:t0 + 1000], w2, rtol=2 * W_TOL_PLAIN_SOFTMAX, atol=1e-37)
+
+
 def test_bf16_logits_with_many_ties():
     for E, k, kw in [(160, 6, dict(n_groups=8, top_groups=3)), (512, 10, {}), (256, 8, dict(n_groups=8, top_groups=4, group_score="sum2"))]:
         t = torch.from_numpy(logits_of(400, E, 9)).cuda().to(torch.bfloat16)
@@ -125,6 +159,7 @@ def test_masked_and_extreme_logits():
     rows[5] = np.finfo(np.float32).min
     rows[6, 7] = np.inf
     rows[7, [9, 4]] = np.inf
+    rows[7, 2] = np.finfo(np.float32).max
     rows[8, ::2] = np.nan
     rows[9] = 0.0
     rows[10] = -200 + base[10]   # every sigmoid below fp32's smallest
@@ -144,9 +179,22 @@ def test_masked_and_extreme_logits():
     check(base, k, bias, score="sigmoid")
     bias[11] = np.inf
     check(base, k, bias, score="softmax", n_groups=8, top_groups=4, group_score="sum2")
+    rows[15, 20:] = -np.inf
+    rows[15, :3] = np.nan
+    check(rows[15:], k, None, score="sigmoid", n_groups=8, top_groups=4, group_score="sum2")
+    check(rows[15:], k, None, score="softmax", n_groups=8, top_groups=4, group_score="sum2")
     huge = np.zeros(E, np.float32)
     huge[::3] = 3e38
     check(base, k, huge, score="sigmoid")
+
+
+def test_zeros_of_either_sign_tie():
+    l = np.full((3, 64), -1.0, np.float32)
+    l[:, [3, 10, 11, 40]] = [0.0, -0.0, 0.0, -0.0]
+    l[1] = -l[1] * 0
+    for bias in (None, np.zeros(64, np.float32)):
+        check(l, 4, bias)
+        check(l, 2, bias, score="sigmoid", n_groups=4, top_groups=2)
 
 
 def test_near_ties_are_decided_in_64_bits():
