@@ -372,7 +372,8 @@ bool use_decode_path(strata_moe_t h, int T) {
 // batch it supports.
 bool use_fused_path(strata_moe_t h, int T) {
     if (h->path == 3) return true;
-    return h->path == 0 && !h->has_rule && T <= h->decode_max_t && fused_decode_supported(h->geo, T);
+    return h->path == 0 && T <= h->decode_max_t && fused_decode_supported(h->geo, T) &&
+           (!h->has_rule || fused_rule_supported(h->rule));
 }
 
 // The whole layer in one launch (router, top-k, dispatch, experts, combine).
@@ -381,8 +382,9 @@ strata_status run_forward_fused(strata_moe_t h, const void *x, int T, void *y, b
     const Geometry &g = h->geo;
     if (!fused_decode_supported(g, T))
         return fail(STRATA_ERR_INVALID_ARG, "the fused decode kernel does not support T=%d", T);
-    if (h->has_rule)
-        return fail(STRATA_ERR_INVALID_ARG, "the fused decode kernel does not take a routing rule");
+    if (h->has_rule && !fused_rule_supported(h->rule))
+        return fail(STRATA_ERR_INVALID_ARG,
+                    "the fused decode kernel does not support the routing rule's groups");
     ExpertWeights w{h->wq, h->wq + (size_t)g.E * g.expert_bytes};
     FusedArgs fa{};
     fa.x = x;
@@ -405,6 +407,7 @@ strata_status run_forward_fused(strata_moe_t h, const void *x, int T, void *y, b
     fa.cnt_tok = h->fused_tok;
     fa.err = h->err;
     fa.budget = h->budget;
+    fa.rule = h->has_rule ? &h->rule : nullptr;
     probe(h, kStGateUp, true, s);
     cudaError_t ce = launch_fused_decode(g, w, fa, T, s);
     probe(h, kStGateUp, false, s);

@@ -60,6 +60,7 @@
 // error word, lets its copies land and returns.
 #include "common.cuh"
 #include "internal.h"
+#include "select.cuh"
 #include "topk.cuh"
 
 namespace strata {
@@ -78,6 +79,7 @@ constexpr int kDownSlabs = 8;                   // a down block: 8 slabs = 128 r
 constexpr int kFStagedMaxT = 8;                 // token rows kept in shared memory
 constexpr int kFMaxT = 64;                      // most tokens per call
 constexpr int kFMaxK = 16;                      // most routed experts per token
+constexpr int kRuleElements = 16;              // experts of a lane under a routing rule (32 x 16 = 512)
 constexpr int kTopkLocalT = 16;                 // up to here every CTA runs the whole top-k
 constexpr int kPubQ = 64;                       // publish queue entries
 constexpr int kMaxA = 4;                        // activation buffers (one down block each)
@@ -114,6 +116,7 @@ struct FusedParams {
     int cnt_tok;              // (at this offset) finished down blocks per (token, row block)
     int *err;
     long long budget;
+    SelectPlan rule;          // kRule kernels: the routing rule
 };
 
 // Shared-memory carve (host and device agree on it).
@@ -673,7 +676,29 @@ auto last_warp = [&](int slot) -> bool {
     }
     return jpos;
 }
-template <int kBits, bool kStaged>
+
+// Picks of one token by the layer's routing rule (kRule kernels), by one warp:
+// to idx and w.  The logits come from all blocks, so they are read past L1.
+static_assert(kTopkLocalT * (int)sizeof(SelectScratch<32>) <= kGroups * kRedSlot,
+              "the picking warps' scratch lies in the partial-sum area (ring >= kGroups slots)");
+static __device__ __noinline__ void rule_topk(const SelectPlan &rule, const float *row, SelectScratch<32> &scratch,
+                                              int32_t *idx, float *w) {
+    const bool vec = rule.gs % 4 == 0 && ((uintptr_t)row % 16) == 0 && ((uintptr_t)rule.bias % 16) == 0;
+    if (rule.score == STRATA_SCORE_SOFTMAX) {
+        if (rule.bias)
+            select_tokens<32, kRuleElements, true, true>(rule, row, false, vec, 0, 1, 0, nullptr, scratch, idx, w, true);
+        else
+            select_tokens<32, kRuleElements, true, false>(rule, row, false, vec, 0, 1, 0, nullptr, scratch, idx, w, true);
+    } else {
+        if (rule.bias)
+            select_tokens<32, kRuleElements, false, true>(rule, row, false, vec, 0, 1, 0, nullptr, scratch, idx, w, true);
+        else
+            select_tokens<32, kRuleElements, false, false>(rule, row, false, vec, 0, 1, 0, nullptr, scratch, idx, w, true);
+    }
+    __syncwarp();
+}
+
+template <int kBits, bool kStaged, bool kRule>
 __global__ void __launch_bounds__(kFThreads, 1) fused_decode_kernel(const __grid_constant__ FusedParams p) {
     extern __shared__ __align__(128) uint8_t sm[];
     constexpr int UB = unit_bytes(kBits);
@@ -1256,12 +1281,17 @@ __global__ void __launch_bounds__(kFThreads, 1) fused_decode_kernel(const __grid
             if (lane == 0 && ok) ok = fwait(rdy, 0, p, abort_flag) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (ok) {
-                int pe;
-                float pw;
-                warp_topk(p.logits + (size_t)warp * E, E, k, lane, pe, pw);
-                if (lane < k) {
-                    sidx[warp * k + lane] = pe;
-                    sw[warp * k + lane] = pw;
+                if constexpr (kRule) {
+                    rule_topk(p.rule, p.logits + (size_t)warp * E,
+                              reinterpret_cast<SelectScratch<32> *>(red)[warp], sidx + warp * k, sw + warp * k);
+                } else {
+                    int pe;
+                    float pw;
+                    warp_topk(p.logits + (size_t)warp * E, E, k, lane, pe, pw);
+                    if (lane < k) {
+                        sidx[warp * k + lane] = pe;
+                        sw[warp * k + lane] = pw;
+                    }
                 }
             } else if (lane == 0) {
                 misc[kMiscDead] = 1;
@@ -1282,12 +1312,17 @@ __global__ void __launch_bounds__(kFThreads, 1) fused_decode_kernel(const __grid
         compute_sync();
         alive = *cflag != 0;
         if (alive && warp == 0 && cta < T) {
-            int pe;
-            float pw;
-            warp_topk(p.logits + (size_t)cta * E, E, k, lane, pe, pw);
-            if (lane < k) {
-                p.idx[(size_t)cta * k + lane] = pe;
-                p.wts[(size_t)cta * k + lane] = pw;
+            if constexpr (kRule) {
+                rule_topk(p.rule, p.logits + (size_t)cta * E, *reinterpret_cast<SelectScratch<32> *>(red),
+                          p.idx + (size_t)cta * k, p.wts + (size_t)cta * k);
+            } else {
+                int pe;
+                float pw;
+                warp_topk(p.logits + (size_t)cta * E, E, k, lane, pe, pw);
+                if (lane < k) {
+                    p.idx[(size_t)cta * k + lane] = pe;
+                    p.wts[(size_t)cta * k + lane] = pw;
+                }
             }
         }
         __syncwarp();
@@ -1415,6 +1450,15 @@ static bool fused_plan(const Geometry &g, int T, FusedPlan &pl) {
     return pl.ring >= min_ring;
 }
 
+template <bool kRule>
+static auto fused_kernel(int bits, bool staged) {
+    return bits == 1   ? (staged ? fused_decode_kernel<1, true, kRule> : fused_decode_kernel<1, false, kRule>)
+           : bits == 2 ? (staged ? fused_decode_kernel<2, true, kRule> : fused_decode_kernel<2, false, kRule>)
+                       : (staged ? fused_decode_kernel<3, true, kRule> : fused_decode_kernel<3, false, kRule>);
+}
+
+bool fused_rule_supported(const SelectPlan &rule) { return lane_elements(rule, 32) <= kRuleElements; }
+
 int fused_decode_supported(const Geometry &g, int T) {
     FusedPlan pl;
     return fused_plan(g, T, pl) ? 1 : 0;
@@ -1464,9 +1508,8 @@ cudaError_t launch_fused_decode(const Geometry &g, const ExpertWeights &w, const
     p.ring = pl.ring;
     const int smem = fused_smem(T, g.E, g.k, g.H, g.Ip, p.ring, p.item_bytes, p.staged, p.units_max,
                                 p.na).total;
-    auto kern = g.bits == 1   ? (p.staged ? fused_decode_kernel<1, true> : fused_decode_kernel<1, false>)
-                : g.bits == 2 ? (p.staged ? fused_decode_kernel<2, true> : fused_decode_kernel<2, false>)
-                              : (p.staged ? fused_decode_kernel<3, true> : fused_decode_kernel<3, false>);
+    auto kern = fa.rule ? fused_kernel<true>(g.bits, p.staged) : fused_kernel<false>(g.bits, p.staged);
+    if (fa.rule) p.rule = *fa.rule;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(G);
     cfg.blockDim = dim3(kFThreads);
@@ -1487,14 +1530,13 @@ cudaError_t fused_init_attributes(int max_smem) {
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&g_fused_sms, cudaDevAttrMultiProcessorCount, dev);
     cudaError_t e;
-    if ((e = allow_max_dyn_smem(fused_decode_kernel<1, true>, max_smem)) != cudaSuccess) return e;
-    if ((e = allow_max_dyn_smem(fused_decode_kernel<1, false>, max_smem)) != cudaSuccess) return e;
-    if ((e = allow_max_dyn_smem(fused_decode_kernel<2, true>, max_smem)) != cudaSuccess) return e;
-    if ((e = allow_max_dyn_smem(fused_decode_kernel<2, false>, max_smem)) != cudaSuccess) return e;
-    if ((e = allow_max_dyn_smem(fused_decode_kernel<3, true>, max_smem)) != cudaSuccess) return e;
-    if ((e = allow_max_dyn_smem(fused_decode_kernel<3, false>, max_smem)) != cudaSuccess) return e;
+    for (int bits = 1; bits <= 3; bits++)
+        for (int staged = 0; staged < 2; staged++) {
+            if ((e = allow_max_dyn_smem(fused_kernel<false>(bits, staged), max_smem)) != cudaSuccess) return e;
+            if ((e = allow_max_dyn_smem(fused_kernel<true>(bits, staged), max_smem)) != cudaSuccess) return e;
+        }
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void *>(fused_decode_kernel<2, true>))) !=
+    if ((e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void *>(fused_decode_kernel<2, true, false>))) !=
         cudaSuccess)
         return e;
     g_fused_max_smem = max_smem - (int)fa.sharedSizeBytes;

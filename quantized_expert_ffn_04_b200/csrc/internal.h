@@ -177,8 +177,11 @@ struct FusedArgs {
     int cnt_tok;                // max_units(64, k, E, 8): per-unit counters come first
     int *err;
     long long budget;
+    const SelectPlan *rule;     // the layer's routing rule, or null (host pointer, read by the launch)
 };
 int fused_decode_supported(const Geometry &g, int T);
+// Whether the kernel's picking warps hold the rule's groups (at most 16 experts a lane).
+bool fused_rule_supported(const SelectPlan &rule);
 cudaError_t launch_fused_decode(const Geometry &g, const ExpertWeights &w, const FusedArgs &a,
                                 int T, cudaStream_t s);
 cudaError_t fused_init_attributes(int max_smem);

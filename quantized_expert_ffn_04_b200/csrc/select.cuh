@@ -40,10 +40,12 @@ constexpr float kSumTol = 1.5e-7f;  // of |v|: two roundings of 2^-24, padded
 struct LogitRow {
     const void *p;
     bool bf16;
+    bool cg = false;  // written by this kernel's other blocks: read past L1
     // Logit e as the rule reads it: -inf for an expert that is not eligible (NaN
     // or -inf), +inf as the largest finite float.
     __device__ __forceinline__ float at(int e) const { return clean(raw(e)); }
     __device__ __forceinline__ float raw(int e) const {
+        if (cg) return __ldcg(reinterpret_cast<const float *>(p) + e);
         return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[e])
                     : reinterpret_cast<const float *>(p)[e];
     }
@@ -51,7 +53,7 @@ struct LogitRow {
     __device__ __forceinline__ LogitRow of_lane(int src) const {
         return LogitRow{reinterpret_cast<const void *>(
                             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src)),
-                        bf16};
+                        bf16, cg};
     }
     static __device__ __forceinline__ float clean(float l) {
         return l == l ? fminf(l, FLT_MAX) : -INFINITY;
@@ -241,7 +243,8 @@ __device__ __forceinline__ void load_four(LogitRow row, bool vec, const SelectLa
     const int at = sl.first + (i >> 2) * sl.step;
     if (vec && !row.bf16) {
         float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (sl.valid(i)) u = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(row.p) + at);
+        const float4 *q = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(row.p) + at);
+        if (sl.valid(i)) u = row.cg ? __ldcg(q) : *q;
         f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
     } else if (vec) {
         uint2 u = make_uint2(0, 0);
@@ -266,7 +269,7 @@ __device__ __forceinline__ void load_all(LogitRow row, bool vec, const SelectLan
 template <int NQ>
 __device__ __forceinline__ void load_elements(LogitRow row, bool vec, const SelectLanes &sl, float (&v)[NQ]) {
     // one branch round all the loads
-    if (vec && !row.bf16) load_all<NQ>(LogitRow{row.p, false}, true, sl, v);
+    if (vec && !row.bf16) load_all<NQ>(LogitRow{row.p, false, row.cg}, true, sl, v);
     else if (vec) load_all<NQ>(LogitRow{row.p, true}, true, sl, v);
     else load_all<NQ>(row, false, sl, v);
 }
@@ -375,14 +378,15 @@ __device__ __forceinline__ SelectLanes lanes_of(const SelectPlan &p, int r, int 
 template <int S, int NQ, bool kSoftmax, bool kBias>
 __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *logits, bool bf16, bool vec,
                                               long long ld, int T, long long t0, const float4 *bias,
-                                              SelectScratch<S> &scratch, int32_t *idx, float *w) {
+                                              SelectScratch<S> &scratch, int32_t *idx, float *w,
+                                              bool cg = false) {
     constexpr int kCap = SelectScratch<S>::kCap, kOwn = kCap / S;
     constexpr bool kTwo = S < 32;  // the threshold from every lane's best two
     constexpr unsigned kAll = 0xffffffffu, kSub = S == 32 ? kAll : (1u << (S & 31)) - 1u;
     const int lane = threadIdx.x & 31, r = lane % S, base = lane - r;
     const long long t = t0 + lane / S < T ? t0 + lane / S : T - 1;
     const bool live = t0 + lane / S < T;
-    const LogitRow row{reinterpret_cast<const char *>(logits) + t * ld * (bf16 ? 2 : 4), bf16};
+    const LogitRow row{reinterpret_cast<const char *>(logits) + t * ld * (bf16 ? 2 : 4), bf16, cg};
     const bool grouped = p.top_groups < p.n_groups;
     const bool group_scores = !kBias && grouped && p.sum2;
     const int ll = (S == 32 ? 5 : S == 16 ? 4 : 3) - p.log2_groups, g = r >> ll;

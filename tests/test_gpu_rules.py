@@ -346,6 +346,49 @@ def test_layer_forward_by_its_rule(shape, T, kw):
     L.close()
 
 
+@pytest.mark.parametrize("kw", LAYER_RULES + [dict(score="sigmoid", renorm=False), dict(score="softmax", n_groups=8, top_groups=2)],
+                         ids=["sigmoid-groups", "softmax-plain", "sigmoid-plain", "softmax-groups"])
+@pytest.mark.parametrize("shape,T", [(gen.TINY, 3), (gen.TINY, 9), (gen.TINY, 17), (gen.TINY, 64), (gen.FLASH2, 1), (gen.FLASH2, 4),
+                                     (gen.FLASH2, 16), (gen.FLASH2, 64), (gen.FLASH3, 8), (gen.CODER1, 5)],
+                         ids=["tiny-3", "tiny-9", "tiny-17", "tiny-64", "flash2-1", "flash2-4", "flash2-16", "flash2-64", "flash3-8", "coder1-5"])
+def test_single_launch_decode_by_rule(shape, T, kw):
+    """The fused decode kernel picks by the rule too: one launch, and the kernel
+    chain's output on the same routing within the layer tolerance."""
+    for bias in (True, False):
+        layer, L, sb = layer_with_rule(shape, T, kw, seed=4, bias=bias)
+        x = to_dev_bf16(gen.hidden(T, shape.hidden, seed=12))
+        L.set_option(qe.STRATA_OPT_PATH, 3)
+        assert qe.strata_moe_launch_count(L.handle, T) == 1
+        y = L.forward(x)
+        assert torch.equal(L.forward(x), y)
+        L.sync_status()
+        L.set_option(qe.STRATA_OPT_PATH, 1)
+        ref = npref.bf16_bits_to_f64(from_dev_bf16(L.forward(x)))
+        check_output(from_dev_bf16(y), ref)
+        L.sync_status()
+        L.close()
+
+
+def test_rules_the_fused_kernel_does_not_hold_take_the_chain():
+    shape = gen.LayerShape(hidden=256, n_experts=510, top_k=3, inter=128)
+    kw = dict(score="sigmoid", n_groups=17, top_groups=3, group_score="sum2")
+    layer, L, sb = layer_with_rule(shape, 5, kw, seed=1)
+    x = gen.hidden(5, shape.hidden, seed=3)
+    xd = to_dev_bf16(x)
+    assert qe.strata_moe_launch_count(L.handle, 5) == 9
+    y = L.forward(xd)
+    ridx, rw = rule_reference(layer, x, kw, sb)
+    check_output(from_dev_bf16(y), forward_reference(layer, x, ridx, rw, range(5)))
+    L.set_option(qe.STRATA_OPT_PATH, 3)
+    with pytest.raises(qe.StrataError) as e:
+        L.forward(xd)
+    assert e.value.status == qe.STRATA_ERR_INVALID_ARG
+    L.set_option(qe.STRATA_OPT_PATH, 0)
+    assert torch.equal(L.forward(xd), y)
+    L.sync_status()
+    L.close()
+
+
 def test_default_rule_given_explicitly_matches_the_default():
     """softmax, no groups, renormalised: the same picks as without a rule."""
     shape, T = gen.FLASH2, 64
