@@ -269,6 +269,111 @@ def make_routing(score="softmax", n_groups=1, top_groups=None, group_score="best
                               groups[group_score], 1 if renorm else 0, scale)
 
 
+_Q8 = {"e4m3": STRATA_Q8_E4M3, "int8": STRATA_Q8_INT8}
+
+
+def _rows(t, name, dtypes, cols=None):
+    """A contiguous [rows, cols] CUDA tensor of one of the dtypes, else ValueError."""
+    if not t.is_cuda or t.dim() != 2 or not t.is_contiguous() or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a contiguous 2-d CUDA tensor of {' or '.join(map(str, dtypes))}")
+    if cols is not None and t.shape[1] != cols:
+        raise ValueError(f"{name} must have {cols} columns")
+    return t.data_ptr()
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def route_logits(logits, rule, k, select_bias=None, stream=None):
+    """Picks int32 [T, k] and weights float32 [T, k] of logits [T, E] (float32 or
+    bfloat16 CUDA tensor; rows may be strided) by a routing rule (make_routing)."""
+    import torch
+    if not logits.is_cuda or logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a 2-d float32 or bfloat16 CUDA tensor")
+    T, E = logits.shape
+    if T and E > 1 and logits.stride(1) != 1 or T > 1 and logits.stride(0) < E:
+        raise ValueError("logits' rows must be contiguous and may not overlap")
+    bias = None
+    if select_bias is not None:
+        _same_device(logits, select_bias)
+        if select_bias.dtype != torch.float32 or select_bias.shape != (E,) or not select_bias.is_contiguous():
+            raise ValueError(f"select_bias must be a contiguous float32 tensor of {E} values")
+        bias = select_bias.data_ptr()
+    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    strata_moe_route_logits(rule, logits.data_ptr(), STRATA_F32 if logits.dtype == torch.float32 else STRATA_BF16,
+                            logits.stride(0) if T > 1 else max(E, 1), bias, T, E, k, idx.data_ptr(), w.data_ptr(),
+                            _stream_ptr(stream))
+    return idx, w
+
+
+def packed_row_bytes(H, group=128) -> int:
+    """Bytes of a packed 8-bit row: H codes, then the scales, up to a multiple of 16."""
+    return H + (4 * (H // group if group else 1) + 15) // 16 * 16
+
+
+def add_rmsnorm(x, delta=None, weight=None, eps=1e-6, quant=None, group=128, want_xn=True, stream=None):
+    """A block's pre-norm of bfloat16 [T, H] rows: h = x + delta, xn = RMSNorm(h)
+    weight.  Returns (h, xn, packed): h is x itself without a delta, xn None
+    unless wanted, packed None or, with quant "e4m3" or "int8", the rows in 8
+    bits as uint8 [T, packed_row_bytes(H, group)] (codes, then float32 scales)."""
+    import torch
+    T, H = x.shape
+    xp = _rows(x, "x", (torch.bfloat16,))
+    _same_device(x, delta, weight)
+    dp = None if delta is None else _rows(delta, "delta", (torch.bfloat16,), H)
+    if delta is not None and delta.shape[0] != T:
+        raise ValueError(f"delta must have {T} rows")
+    if weight is not None and (weight.dtype not in (torch.float32, torch.bfloat16) or weight.shape != (H,)
+                               or not weight.is_contiguous()):
+        raise ValueError(f"weight must be a contiguous float32 or bfloat16 tensor of {H} values")
+    if quant is not None and quant not in _Q8:
+        raise ValueError(f"unknown 8-bit type {quant!r}")
+    h = x if delta is None else torch.empty_like(x)
+    xn = torch.empty_like(x) if want_xn else None
+    packed = scale = None
+    rb = 0
+    if quant is not None:
+        rb = packed_row_bytes(H, group)
+        full = rb == H + 4 * (H // group if group else 1)  # else the padding is zeros
+        packed = (torch.empty if full else torch.zeros)((T, rb), dtype=torch.uint8, device=x.device)
+        scale = packed.data_ptr() + H
+    if T:
+        strata_moe_add_rmsnorm(xp, dp, None if weight is None else weight.data_ptr(),
+                               STRATA_BF16 if weight is not None and weight.dtype == torch.bfloat16 else STRATA_F32,
+                               eps, T, H, None if delta is None else h.data_ptr(), None if xn is None else xn.data_ptr(),
+                               _Q8[quant] if quant else 0, group, None if packed is None else packed.data_ptr(), rb,
+                               scale, rb // 4, _stream_ptr(stream))
+    return h, xn, packed
+
+
+def dequant_rows(packed, H, quant="e4m3", group=128, rows=None, out=None, stream=None):
+    """Packed 8-bit rows (add_rmsnorm) back in bfloat16 [n, H]: row rows[i] (int32
+    CUDA tensor; outside the rows: out's row i stays as it is), or every row."""
+    import torch
+    if quant not in _Q8:
+        raise ValueError(f"unknown 8-bit type {quant!r}")
+    p = _rows(packed, "packed", (torch.uint8,), packed_row_bytes(H, group))
+    n = packed.shape[0]
+    if rows is not None:
+        if rows.dtype != torch.int32 or rows.dim() != 1 or not rows.is_contiguous():
+            raise ValueError("rows must be a contiguous 1-d int32 tensor")
+        n = rows.shape[0]
+    _same_device(packed, rows, out)
+    if out is None:
+        out = torch.empty((n, H), dtype=torch.bfloat16, device=packed.device)
+    op = _rows(out, "out", (torch.bfloat16,), H)
+    if out.shape[0] != n:
+        raise ValueError(f"out must have {n} rows")
+    rb = packed.shape[1]
+    strata_moe_dequant_rows(p, _Q8[quant], rb, p + H, rb // 4, group, None if rows is None else rows.data_ptr(), n,
+                            packed.shape[0], H, op, _stream_ptr(stream))
+    return out
+
+
 def make_config(shape, max_tokens: int) -> strata_moe_config:
     """Config from any object with hidden/n_experts/top_k/inter/bits/router_bias."""
     return strata_moe_config(shape.hidden, shape.n_experts, shape.top_k, shape.inter, shape.bits,

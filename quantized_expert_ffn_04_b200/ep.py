@@ -22,6 +22,12 @@ decode kernel sums its K partials in another order and agrees within the
 layer tolerance).  The exchange is
 torch.distributed's all_to_all_single (NCCL on GPUs, gloo on CPU).
 
+ExpertParallel.forward_block starts a step earlier, at the block's pre-norm
+(strata_moe_add_rmsnorm), and exchanges the normalised rows in 8 bits with
+scales, half of the bf16 bytes: every expert, routed or shared, runs on the
+rows read back from 8 bits (strata_moe_dequant_rows), so that all ranks see the
+same row (its prescale exponent included); the router sees the bf16 rows.
+
 The compute steps go through a backend; GpuBackend calls the library's
 kernels through the C ABI.  Any object with the same methods works (the
 tests drive the exchange logic on CPU ranks with a numpy backend).
@@ -30,12 +36,15 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (Layer, strata_ep_expert_range, strata_ep_gather_rows, strata_ep_plan,
-               strata_moe_combine_rows, strata_moe_expert_rows)
+from . import (Layer, add_rmsnorm, dequant_rows, strata_ep_expert_range, strata_ep_gather_rows,
+               strata_ep_plan, strata_moe_combine_rows, strata_moe_expert_rows)
 
 # decode (the GEMV kernels, fp32 expert outputs) up to this many tokens, like
 # the one-GPU forward's default; the tensor-core kernels (fp16 outputs) above
 DECODE_MAX_T = 64
+
+# the 8-bit form of exchanged rows: e4m3 codes, a scale for every 128 columns
+EXCHANGE_Q8, EXCHANGE_GROUP = "e4m3", 128
 
 
 class GpuBackend:
@@ -77,6 +86,13 @@ class GpuBackend:
         import torch
         return torch.float16 if prefill else torch.float32
 
+    def pre_norm(self, h, delta, weight, eps):
+        """(h + delta, its normalised rows in bf16, the same rows packed in 8 bits)."""
+        return add_rmsnorm(h, delta, weight, eps, quant=EXCHANGE_Q8, group=EXCHANGE_GROUP)
+
+    def unpack_rows(self, packed, out):
+        dequant_rows(packed, self.H, EXCHANGE_Q8, EXCHANGE_GROUP, out=out)
+
 
 def _a2a(out, inp, out_splits, in_splits, group):
     """all_to_all_single that moves bits: 2-byte rows (bf16) travel as fp16,
@@ -104,12 +120,29 @@ class ExpertParallel:
         self.decode_max_t = decode_max_t
 
     def forward(self, x):
+        """The layer's output of the rank's bf16 rows x [T, H]."""
+        idx, w = self.be.route(x)
+        return self._experts(x, idx, w, x)
+
+    def forward_block(self, h, delta, weight, eps=1e-6):
+        """h <- h + delta, then the layer on RMSNorm(h) weight with the exchange in
+        8 bits.  h, delta (or None) bf16 [T, H], weight float32 or bf16 [H] (or
+        None).  Returns (the new h, the layer's output: the next delta)."""
+        import torch
+        h, xn, packed = self.be.pre_norm(h, delta, weight, eps)
+        idx, w = self.be.route(xn)
+        x = torch.empty_like(xn)
+        self.be.unpack_rows(packed, x)
+        return h, self._experts(x, idx, w, packed)
+
+    def _experts(self, x, idx, w, wire):
+        """Exchange, experts and combine of the rank's rows x under its routing;
+        `wire`: the rows as they travel, x itself or packed 8-bit rows."""
         import torch
         import torch.distributed as dist
         T, k, H = x.shape[0], self.k, self.H
         prefill = T > self.decode_max_t
         dev = x.device
-        idx, w = self.be.route(x)
         idx_h = idx.cpu().numpy().reshape(T, k)
         counts, pick, slot = strata_ep_plan(idx_h, self.E, self.world)
         send_counts = torch.from_numpy(counts.astype(np.int64))
@@ -122,14 +155,20 @@ class ExpertParallel:
         n_recv = sum(rc)
         tok_t = torch.from_numpy((pick // k).astype(np.int32)).to(dev)
         # the picked rows and their expert ids, in plan order
-        send_rows = self.be.gather_rows(x, tok_t)
+        send_rows = self.be.gather_rows(wire, tok_t)
         send_ids = torch.from_numpy(idx_h.reshape(-1)[pick].astype(np.int32)).to(dev)
         # own rows first (the shared expert, no routed pick: id -1), then the
         # rows received for this rank's experts
         rows = torch.empty((T + n_recv, H), dtype=x.dtype, device=dev)
         ids = torch.full((T + n_recv,), -1, dtype=torch.int32, device=dev)
         rows[:T].copy_(x)
-        _a2a(rows[T:], send_rows, rc, sc, self.group)
+        if wire is x:
+            _a2a(rows[T:], send_rows, rc, sc, self.group)
+        else:
+            recv = torch.empty((n_recv, wire.shape[1]), dtype=wire.dtype, device=dev)
+            _a2a(recv, send_rows, rc, sc, self.group)
+            if n_recv:
+                self.be.unpack_rows(recv, rows[T:])
         _a2a(ids[T:], send_ids, rc, sc, self.group)
         yd = self.be.y_dtype(prefill)
         y_rows = torch.empty((T + n_recv, H), dtype=yd, device=dev)

@@ -134,3 +134,13 @@ def test_dequant_rows_no_ops_and_host_memory():
     p = a.ctypes.data + (-a.ctypes.data) % 16
     with pytest.raises(qe.StrataError, match="not device memory"):
         dequant(q=p)
+
+
+def test_tensor_functions_refuse_host_tensors():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(2, 256, dtype=torch.bfloat16)
+    for bad in [lambda: qe.add_rmsnorm(x), lambda: qe.route_logits(torch.zeros(2, 64), rule(), 4),
+                lambda: qe.dequant_rows(torch.zeros(2, 272, dtype=torch.uint8), 256)]:
+        with pytest.raises(ValueError):
+            bad()
+    assert qe.packed_row_bytes(2560) == 2640 and qe.packed_row_bytes(256, 0) == 272 and qe.packed_row_bytes(6144, 32) == 6912
