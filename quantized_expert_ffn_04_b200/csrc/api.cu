@@ -322,7 +322,10 @@ strata_status run_route(strata_moe_t h, const void *x, int T, int tile, cudaStre
     if (h->has_rule) {
         // a routing rule reads every expert's exact logit, at any T
         probe(h, kStRouter, true, s);
-        launch_router(x, T, g.H, h->router_wp, h->router_b, g.E, h->logits, s);
+        if (T >= kRouterTileMinT)  // the token operand is free until the experts' prescale
+            launch_router_tile(x, T, g.H, h->router_wp, h->router_b, g.E, h->xs, h->logits, s);
+        else
+            launch_router(x, T, g.H, h->router_wp, h->router_b, g.E, h->logits, s);
         probe(h, kStRouter, false, s);
         const int stage = T > kSmallMaxT ? kStDispatch : kStTopk;
         probe(h, stage, true, s);
@@ -493,8 +496,9 @@ int strata_moe_launch_count(strata_moe_t h, int T) {
     // gather), and the combine.
     if (use_fused_path(h, T)) return 1;  // the fused layer kernel
     const bool decode = use_decode_path(h, T);
-    // with a routing rule: router, rule, 3 dispatch kernels, at any T
-    if (h->has_rule) return 5 + 1 + (decode ? 2 : 3) + 1;
+    // with a routing rule: router (large batches reorder the rows first), rule, 3
+    // dispatch kernels
+    if (h->has_rule) return 5 + (T >= kRouterTileMinT) + 1 + (decode ? 2 : 3) + 1;
     if (T <= kSmallMaxT) return 2 + 1 + (decode ? 2 : 3) + 1;
     return 6 + 1 + 3 + 1;
 }

@@ -178,6 +178,7 @@ cudaError_t init_kernel_attributes() {
     e = cudaDeviceGetAttribute(&max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e != cudaSuccess) return e;
     if ((e = route_init_attributes(max_smem)) != cudaSuccess) return e;
+    if ((e = route_tile_init_attributes(max_smem)) != cudaSuccess) return e;
     if ((e = gemv_init_attributes(max_smem)) != cudaSuccess) return e;
     if ((e = umma_init_attributes(max_smem)) != cudaSuccess) return e;
     if ((e = fused_init_attributes(max_smem)) != cudaSuccess) return e;

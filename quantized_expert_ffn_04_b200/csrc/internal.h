@@ -86,6 +86,16 @@ void launch_screen_debug(const float *D, int R, const void *x, int T, int H, con
                          int E, float gam, float wmax, float bmax, float *a_out, float *eps_out,
                          cudaStream_t s);
 
+// ---- route_tile.cu
+// The same logits, bit for bit, from tiles of 32 tokens x 32 experts; xi: scratch of
+// T H 2 bytes (16-byte aligned).  From 1024 tokens on it is the faster one (512
+// experts, H = 2560: T = 1024 90 us against 122, T = 8192 606 against 911; T = 300
+// 49 against 48).
+constexpr int kRouterTileMinT = 1024;
+void launch_router_tile(const void *x, int T, int H, const float *Wp, const float *bias, int E, void *xi,
+                        float *logits, cudaStream_t s);
+cudaError_t route_tile_init_attributes(int max_smem);
+
 // ---- select.cu (routing rules)
 // A routing rule checked against a layer's or a call's sizes.
 struct SelectPlan {

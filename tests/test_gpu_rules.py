@@ -281,8 +281,9 @@ def rule_reference(layer, x_bits, kw, sb):
 
 
 @pytest.mark.parametrize("kw", LAYER_RULES, ids=["sigmoid-groups", "softmax-plain"])
-@pytest.mark.parametrize("shape,T", [(gen.TINY, 1), (gen.TINY, 8), (gen.TINY, 70), (gen.FLASH2, 4), (gen.FLASH2, 300)],
-                         ids=["tiny-1", "tiny-8", "tiny-70", "flash-4", "flash-300"])
+@pytest.mark.parametrize("shape,T", [(gen.TINY, 1), (gen.TINY, 8), (gen.TINY, 70), (gen.TINY, 1025), (gen.FLASH2, 4), (gen.FLASH2, 300), (gen.FLASH2, 1100),
+                                     (gen.LayerShape(hidden=384, n_experts=40, top_k=3, inter=32, router_bias=True), 1031)],
+                         ids=["tiny-1", "tiny-8", "tiny-70", "tiny-1025", "flash-4", "flash-300", "flash-1100", "odd-1031"])
 def test_layer_routes_by_its_rule(shape, T, kw):
     layer, L, sb = layer_with_rule(shape, T, kw)
     x = gen.hidden(T, shape.hidden, seed=5)
@@ -320,15 +321,15 @@ def forward_reference(layer, x_bits, idx, w, tokens):
 
 
 @pytest.mark.parametrize("kw", LAYER_RULES, ids=["sigmoid-groups", "softmax-plain"])
-@pytest.mark.parametrize("shape,T", [(gen.TINY, 1), (gen.TINY, 9), (gen.TINY, 70), (gen.TINY, 300), (gen.FLASH2, 4)],
-                         ids=["tiny-1", "tiny-9", "tiny-70", "tiny-300", "flash-4"])
+@pytest.mark.parametrize("shape,T", [(gen.TINY, 1), (gen.TINY, 9), (gen.TINY, 70), (gen.TINY, 300), (gen.TINY, 1100), (gen.FLASH2, 4)],
+                         ids=["tiny-1", "tiny-9", "tiny-70", "tiny-300", "tiny-1100", "flash-4"])
 def test_layer_forward_by_its_rule(shape, T, kw):
     layer, L, sb = layer_with_rule(shape, T, kw, seed=2)
     x = gen.hidden(T, shape.hidden, seed=6)
     xd = to_dev_bf16(x)
     y = L.forward(xd)
     ridx, rw = rule_reference(layer, x, kw, sb)
-    tokens = list(range(T)) if shape is gen.TINY else [0, T - 1]
+    tokens = list(range(T))[::max(1, T // 100)] if shape is gen.TINY else [0, T - 1]
     check_output(from_dev_bf16(y)[tokens], forward_reference(layer, x, ridx, rw, tokens))
     assert torch.equal(L.forward(xd), y), "two forwards differ"
     # a captured forward keeps working on new tokens
