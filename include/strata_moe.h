@@ -172,7 +172,8 @@ typedef struct {
  *   logits_dev      [T][ld] (device), the first E of every row read; bf16 or
  *                   float as logits_type says; ld >= E
  *   select_bias_dev float [E] (device) or NULL
- *   idx_dev int32 [T][k], w_dev float [T][k] out (device)
+ *   idx_dev int32 [T][k], w_dev float [T][k] out (device); they overlap
+ *                   neither each other nor an input
  * 1 <= E <= 1024, 1 <= k <= min(E, 32).  Runs on the device that holds
  * logits_dev, whichever is current; `stream` belongs to that device.  No
  * workspace: calls on different streams may overlap.  T == 0 is a no-op. */

@@ -319,7 +319,8 @@ def add_rmsnorm(x, delta=None, weight=None, eps=1e-6, quant=None, group=128, wan
     """A block's pre-norm of bfloat16 [T, H] rows: h = x + delta, xn = RMSNorm(h)
     weight.  Returns (h, xn, packed): h is x itself without a delta, xn None
     unless wanted, packed None or, with quant "e4m3" or "int8", the rows in 8
-    bits as uint8 [T, packed_row_bytes(H, group)] (codes, then float32 scales)."""
+    bits as uint8 [T, packed_row_bytes(H, group)] (codes, then float32 scales; the
+    bytes behind them are not written)."""
     import torch
     T, H = x.shape
     xp = _rows(x, "x", (torch.bfloat16,))
@@ -338,8 +339,7 @@ def add_rmsnorm(x, delta=None, weight=None, eps=1e-6, quant=None, group=128, wan
     rb = 0
     if quant is not None:
         rb = packed_row_bytes(H, group)
-        full = rb == H + 4 * (H // group if group else 1)  # else the padding is zeros
-        packed = (torch.empty if full else torch.zeros)((T, rb), dtype=torch.uint8, device=x.device)
+        packed = torch.empty((T, rb), dtype=torch.uint8, device=x.device)
         scale = packed.data_ptr() + H
     if T:
         strata_moe_add_rmsnorm(xp, dp, None if weight is None else weight.data_ptr(),

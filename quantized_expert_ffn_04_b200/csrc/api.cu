@@ -473,6 +473,15 @@ strata_status run_forward(strata_moe_t h, const void *x, int T, void *y, bool re
 
 void strata::set_error_message(const char *msg) { g_err = msg; }
 
+strata_status strata::refuse(const char *who, const char *what) {
+    return fail(STRATA_ERR_INVALID_ARG, "%s: %s", who, what);
+}
+
+strata_status strata::launched(const char *who, cudaError_t e) {
+    if (e == cudaSuccess) return STRATA_OK;
+    return fail(STRATA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+}
+
 extern "C" {
 
 const char *strata_moe_last_error(void) { return g_err.c_str(); }
@@ -711,6 +720,8 @@ strata_status strata_moe_set_routing(strata_moe_t h, const strata_moe_routing *r
         if (!h->select_bias && dev_malloc(&h->select_bias, bytes) != cudaSuccess)
             return fail(STRATA_ERR_OOM, "selection bias allocation failed");
         ce = cudaMemcpy(h->select_bias, select_bias, bytes, cudaMemcpyHostToDevice);
+        // a small copy may return before it lands; later calls use any stream
+        if (ce == cudaSuccess) ce = cudaDeviceSynchronize();
         if (ce != cudaSuccess) return cuda_fail(ce, "selection bias upload");
         plan.bias = h->select_bias;
     }
@@ -826,6 +837,9 @@ strata_status strata_moe_stack_forward(const strata_moe_t *layers, int n_layers,
             L->cfg.n_experts != l0->cfg.n_experts || L->cfg.top_k != l0->cfg.top_k ||
             L->cfg.inter != l0->cfg.inter || L->cfg.quant_bits != l0->cfg.quant_bits)
             return fail(STRATA_ERR_INVALID_ARG, "layer %d does not match layer 0", l);
+        if (l0->path == 3 && L->has_rule && !fused_rule_supported(L->rule))
+            return fail(STRATA_ERR_INVALID_ARG,
+                        "the fused decode kernel does not support the routing rule of layer %d", l);
     }
     DeviceGuard guard(l0->device);
     cudaStream_t s = (cudaStream_t)stream;

@@ -229,6 +229,22 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// A refusal of the entry point `who`: sets the message, returns the status.
+strata_status refuse(const char *who, const char *what);
+// A launch's outcome as the entry point's status.
+strata_status launched(const char *who, cudaError_t e);
+
+// A caller's buffer of `rows` rows of `bytes` bytes, `stride` bytes apart.
+struct Span {
+    uintptr_t begin = 0, end = 0;
+    Span(const void *p, long long rows, long long stride, long long bytes) {
+        if (!p || rows <= 0) return;
+        begin = (uintptr_t)p;
+        end = begin + (uintptr_t)((rows - 1) * stride + bytes);
+    }
+    bool meets(const Span &o) const { return begin < o.end && o.begin < end; }
+};
+
 // The device that holds `p` becomes current for the scope of a call without a
 // handle; ok is false when p is not device memory.
 struct PointerDevice {

@@ -8,7 +8,6 @@
 // Both kernels are one pass over HBM.
 #include <float.h>
 #include <math.h>
-#include <stdio.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -346,32 +345,6 @@ static cudaError_t launch_dequant_rows(const DequantArgs &a, int q8, cudaStream_
     return launch_pdl(q8 == STRATA_Q8_INT8 ? dequant_rows_kernel<STRATA_Q8_INT8> : dequant_rows_kernel<STRATA_Q8_E4M3>,
                       grid, dim3(32 * kDequantWarps), 0, s, a);
 }
-
-// A call's refusal: message and status.
-static strata_status refuse(const char *who, const char *what) {
-    char buf[256];
-    snprintf(buf, sizeof buf, "%s: %s", who, what);
-    set_error_message(buf);
-    return STRATA_ERR_INVALID_ARG;
-}
-static strata_status launched(const char *who, cudaError_t e) {
-    if (e == cudaSuccess) return STRATA_OK;
-    char buf[256];
-    snprintf(buf, sizeof buf, "%s: %s", who, cudaGetErrorString(e));
-    set_error_message(buf);
-    return STRATA_ERR_CUDA;
-}
-
-// A caller's buffer of `rows` rows of `bytes` bytes, `stride` bytes apart.
-struct Span {
-    uintptr_t begin = 0, end = 0;
-    Span(const void *p, long long rows, long long stride, long long bytes) {
-        if (!p || rows <= 0) return;
-        begin = (uintptr_t)p;
-        end = begin + (uintptr_t)((rows - 1) * stride + bytes);
-    }
-    bool meets(const Span &o) const { return begin < o.end && o.begin < end; }
-};
 
 static const char *bad_group(int q8, int group, int H) {
     if (q8 != STRATA_Q8_E4M3 && q8 != STRATA_Q8_INT8) return "q8 must be STRATA_Q8_E4M3 or STRATA_Q8_INT8";

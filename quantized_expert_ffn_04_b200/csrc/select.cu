@@ -7,7 +7,6 @@
 // with a bias) take 39 us, 479 instructions a token at 66 % of the issue slots,
 // where the read alone would take 11; without groups and bias 23 us.
 #include <math.h>
-#include <stdio.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -32,7 +31,6 @@ cudaError_t launch_route_logits(const SelectPlan &p, const void *logits, bool bf
 
 strata_status make_select_plan(const strata_moe_routing *rule, int E, int k, const char *who,
                                SelectPlan *plan) {
-    char buf[256];
     const char *what = nullptr;
     if (!rule)
         what = "rule is NULL";
@@ -52,11 +50,7 @@ strata_status make_select_plan(const strata_moe_routing *rule, int E, int k, con
         what = "top_groups groups hold fewer than k experts";
     else if (rule->group_score == STRATA_GROUP_SUM2 && E / rule->n_groups < 2)
         what = "STRATA_GROUP_SUM2 needs groups of at least two experts";
-    if (what) {
-        snprintf(buf, sizeof buf, "%s: %s", who, what);
-        set_error_message(buf);
-        return STRATA_ERR_INVALID_ARG;
-    }
+    if (what) return refuse(who, what);
     SelectPlan p{};
     p.E = E;
     p.k = k;
@@ -83,37 +77,29 @@ extern "C" strata_status strata_moe_route_logits(const strata_moe_routing *rule,
                                                  int64_t ld, const float *select_bias_dev, int T,
                                                  int E, int k, int32_t *idx_dev, float *w_dev,
                                                  void *stream) {
-    auto bad = [](const char *what) {
-        char buf[256];
-        snprintf(buf, sizeof buf, "strata_moe_route_logits: %s", what);
-        set_error_message(buf);
-        return STRATA_ERR_INVALID_ARG;
-    };
+    static const char *const who = "strata_moe_route_logits";
     if (T < 0 || E < 1 || E > 1024 || k < 1 || k > 32 || k > E)
-        return bad("need T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 32)");
+        return refuse(who, "need T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 32)");
     if (logits_type != STRATA_BF16 && logits_type != STRATA_F32)
-        return bad("logits_type must be STRATA_BF16 or STRATA_F32");
-    if (ld < E) return bad("ld must be at least E");
+        return refuse(who, "logits_type must be STRATA_BF16 or STRATA_F32");
+    if (ld < E) return refuse(who, "ld must be at least E");
     SelectPlan plan;
-    const strata_status st = make_select_plan(rule, E, k, "strata_moe_route_logits", &plan);
+    const strata_status st = make_select_plan(rule, E, k, who, &plan);
     if (st != STRATA_OK) return st;
     if (T == 0) return STRATA_OK;
-    if (!logits_dev || !idx_dev || !w_dev) return bad("NULL device pointer");
+    if (!logits_dev || !idx_dev || !w_dev) return refuse(who, "NULL device pointer");
     const bool bf16 = logits_type == STRATA_BF16;
     if (((uintptr_t)logits_dev % (bf16 ? 2 : 4)) || ((uintptr_t)select_bias_dev % 4) ||
         ((uintptr_t)idx_dev % 4) || ((uintptr_t)w_dev % 4))
-        return bad("misaligned device pointer");
-    if (ld > (INT64_MAX / 4) / T) return bad("T * ld is too large");
+        return refuse(who, "misaligned device pointer");
+    if (ld > (INT64_MAX / 4) / T) return refuse(who, "T * ld is too large");
+    const int size = bf16 ? 2 : 4;
+    const Span in(logits_dev, T, ld * size, (long long)E * size), sb(select_bias_dev, 1, 0, 4ll * E);
+    const Span is(idx_dev, 1, 0, 4ll * T * k), ws(w_dev, 1, 0, 4ll * T * k);
+    if (is.meets(in) || is.meets(sb) || ws.meets(in) || ws.meets(sb) || is.meets(ws))
+        return refuse(who, "an output overlaps another buffer");
     const PointerDevice on(logits_dev);
-    if (!on.ok) return bad("logits_dev is not device memory");
+    if (!on.ok) return refuse(who, "logits_dev is not device memory");
     plan.bias = select_bias_dev;
-    const cudaError_t e = launch_route_logits(plan, logits_dev, bf16, ld, T, idx_dev, w_dev,
-                                              (cudaStream_t)stream);
-    if (e != cudaSuccess) {
-        char buf[256];
-        snprintf(buf, sizeof buf, "strata_moe_route_logits: %s", cudaGetErrorString(e));
-        set_error_message(buf);
-        return STRATA_ERR_CUDA;
-    }
-    return STRATA_OK;
+    return launched(who, launch_route_logits(plan, logits_dev, bf16, ld, T, idx_dev, w_dev, (cudaStream_t)stream));
 }

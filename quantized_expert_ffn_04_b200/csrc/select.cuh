@@ -90,9 +90,9 @@ static __device__ __noinline__ double score64(const SelectPlan &p, float l, floa
 }
 // Ranking value; -inf for an expert that is not eligible.
 __device__ __forceinline__ double value64(const SelectPlan &p, float l, int e, float m, double inv_z) {
-    if (!p.bias) return (double)l;
+    if (!p.bias || !(l > -INFINITY)) return (double)l;
     const double v = score64(p, l, m, inv_z) + (double)p.bias[e];
-    return l > -INFINITY && v == v ? v : -(double)INFINITY;
+    return v == v ? v : -(double)INFINITY;
 }
 
 // The picks one after the other, from all experts of the kept groups: for

@@ -141,18 +141,21 @@ class ExpertParallel:
         import torch
         import torch.distributed as dist
         T, k, H = x.shape[0], self.k, self.H
-        prefill = T > self.decode_max_t
         dev = x.device
         idx_h = idx.cpu().numpy().reshape(T, k)
         counts, pick, slot = strata_ep_plan(idx_h, self.E, self.world)
-        send_counts = torch.from_numpy(counts.astype(np.int64))
+        # to every rank: the picks it gets, and this rank's token count
+        send_counts = torch.from_numpy(np.stack([counts, np.full_like(counts, T)], 1).astype(np.int64))
         recv_counts = torch.empty_like(send_counts)
         if dev.type == "cuda":
             send_counts, recv_counts = send_counts.to(dev), recv_counts.to(dev)
         dist.all_to_all_single(recv_counts, send_counts, group=self.group)
-        sc = [int(c) for c in send_counts.cpu()]
-        rc = [int(c) for c in recv_counts.cpu()]
+        sc = [int(c) for c in counts]
+        got = recv_counts.cpu()
+        rc = [int(c) for c in got[:, 0]]
         n_recv = sum(rc)
+        # one path on every rank, as the exchanged outputs have its type
+        prefill = int(got[:, 1].max()) > self.decode_max_t
         tok_t = torch.from_numpy((pick // k).astype(np.int32)).to(dev)
         # the picked rows and their expert ids, in plan order
         send_rows = self.be.gather_rows(wire, tok_t)

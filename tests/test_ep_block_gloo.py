@@ -24,6 +24,10 @@ class BlockBackend(NumpyBackend):
 
     wire_bytes = 0
 
+    def y_dtype(self, prefill):
+        self.prefill = prefill
+        return super().y_dtype(prefill)
+
     def gather_rows(self, src, rows):
         if src.dtype == torch.uint8:
             self.wire_bytes += rows.numel() * src.shape[1]
@@ -78,13 +82,13 @@ def _worker(rank, world, port, Ts, out):
         be = BlockBackend(gen.layer_weights(gen.TINY, seed=0))
         ep = ExpertParallel(be, gen.TINY.n_experts, gen.TINY.top_k, gen.TINY.hidden)
         h, y = ep.forward_block(*_inputs(gen.TINY, Ts[rank], rank))
-        out[rank] = (_bits(h).copy(), _bits(y).copy(), be.wire_bytes)
+        out[rank] = (_bits(h).copy(), _bits(y).copy(), be.wire_bytes, be.prefill)
         dist.barrier()
     finally:
         dist.destroy_process_group()
 
 
-@pytest.mark.parametrize("world,Ts", [(2, (8, 8)), (3, (5, 1, 9)), (2, (3, 0))], ids=["2x8", "5-1-9", "3-0"])
+@pytest.mark.parametrize("world,Ts", [(2, (8, 8)), (3, (5, 1, 9)), (2, (3, 0)), (2, (70, 3))], ids=["2x8", "5-1-9", "3-0", "70-3"])
 def test_block_matches_one_rank(world, Ts):
     port = _free_port()
     with mp.Manager() as m:
@@ -92,6 +96,8 @@ def test_block_matches_one_rank(world, Ts):
         mp.spawn(_worker, args=(world, port, Ts, out), nprocs=world, join=True)
         res = dict(out)
     be = BlockBackend(gen.layer_weights(gen.TINY, seed=0))
+    # one path everywhere: the outputs that travel have its type
+    assert all(res[r][3] == (max(Ts) > 64) for r in range(world))
     for r in range(world):
         if not Ts[r]:
             assert res[r][1].size == 0

@@ -23,7 +23,7 @@ def rule(**kw):
     return qe.make_routing(**kw)
 
 
-def route(r, logits=P, typ=qe.STRATA_F32, ld=64, bias=None, T=4, E=64, k=4, idx=P, w=P):
+def route(r, logits=P, typ=qe.STRATA_F32, ld=64, bias=None, T=4, E=64, k=4, idx=8 * P, w=9 * P):
     qe.strata_moe_route_logits(r, logits, typ, ld, bias, T, E, k, idx, w)
 
 
@@ -31,7 +31,8 @@ def route(r, logits=P, typ=qe.STRATA_F32, ld=64, bias=None, T=4, E=64, k=4, idx=
     dict(T=-1), dict(E=0, ld=64), dict(E=1025, ld=1025), dict(k=0), dict(k=33), dict(E=4, k=5),
     dict(typ=2), dict(ld=63), dict(logits=None), dict(idx=None), dict(w=None),
     dict(logits=P + 2), dict(logits=P + 1, typ=qe.STRATA_BF16), dict(bias=P + 2), dict(idx=P + 1),
-    dict(w=P + 3), dict(ld=1 << 61),
+    dict(w=P + 3), dict(ld=1 << 61), dict(idx=P + 64), dict(w=P + 960), dict(idx=8 * P, w=8 * P + 60), dict(bias=16 * P, w=16 * P),
+    dict(bias=8 * P + 60),
 ], ids=str)
 def test_route_logits_refuses(kw):
     refused(lambda: route(rule(), **kw))

@@ -125,6 +125,22 @@ def test_large_batches(E, k, n, top):
                     np.testing.assert_allclose(w[t0:t0 + 1000], w2, rtol=2 * W_TOL_PLAIN_SOFTMAX, atol=1e-37)
 
 
+@pytest.mark.parametrize("T", [9000, 20000])
+def test_large_batches_with_odd_biases(T):
+    """Biases that are not finite, and rows masked with the type's lowest value."""
+    E, k = 128, 6
+    l = logits_of(T, E, T)
+    l[::7, 40:] = np.finfo(np.float32).min
+    bias = bias_of(E, 9)
+    bias[[3, 8, 50]] = [np.nan, -np.inf, np.inf]
+    sample = np.r_[0:64, T - 40:T]
+    for kw in [dict(score="sigmoid"), dict(score="softmax"), dict(score="sigmoid", n_groups=8, top_groups=3, group_score="sum2")]:
+        idx, w = call(l, k, bias, **kw)
+        ridx, rw = route_rule(l[sample], k, bias=bias, **kw)
+        assert np.array_equal(idx[sample], ridx)
+        np.testing.assert_allclose(w[sample], rw, rtol=W_TOL, atol=1e-37)
+
+
 def test_bf16_logits_with_many_ties():
     for E, k, kw in [(160, 6, dict(n_groups=8, top_groups=3)), (512, 10, {}), (256, 8, dict(n_groups=8, top_groups=4, group_score="sum2"))]:
         t = torch.from_numpy(logits_of(400, E, 9)).cuda().to(torch.bfloat16)
@@ -384,6 +400,16 @@ def test_rules_the_fused_kernel_does_not_hold_take_the_chain():
     with pytest.raises(qe.StrataError) as e:
         L.forward(xd)
     assert e.value.status == qe.STRATA_ERR_INVALID_ARG
+    # a stack refuses before it touches its rows
+    first = qe.Layer(layer, max_tokens=5)
+    first.set_option(qe.STRATA_OPT_PATH, 3)
+    h = xd.clone()
+    with pytest.raises(qe.StrataError) as e:
+        qe.strata_moe_stack_forward([first.handle, L.handle], h.data_ptr(), 5)
+    assert e.value.status == qe.STRATA_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.equal(h, xd)
+    first.close()
     L.set_option(qe.STRATA_OPT_PATH, 0)
     assert torch.equal(L.forward(xd), y)
     L.sync_status()
