@@ -10,19 +10,18 @@
 // values that decide something lie closer than the bound are they computed
 // again in 64 bits.
 //
-// Bounds (the fp32 score of one expert against the real one; ex2.approx is
-// within 2^-22 relative, rcp.approx within 2^-23, and the rounded product l
-// log2(e) moves the exponent by at most 1.5 2^-24 |l|):
-//   sigmoid  s (1 - s) (2^-22 + 1.5 2^-24 |l|) + s (2^-23 + 2^-24)
-//            <= (1 + 0.34 + 3) 2^-24 = 2.6e-7, as s (1 - s) |l| <= 0.224;
-//   softmax  p = exp(l - m) / Z, relative to the largest p: the difference's and
-//            the product's rounding and ex2 give at most (4 + 2.5 * 0.37) 2^-24
-//            (x exp(-x) <= 0.37); Z sums up to 64 + 5 roundings of 2^-24 and its
-//            terms' own relative errors, weighted by the terms: (4 + 2.5 * 7)
-//            2^-24 when the mean of |l - m| under p is at most ln 1024 = 7;
-//            together <= 5.7e-6.
-// The sum v = s + b rounds by 2^-24 |v|.  kSigmoidTol and kSoftmaxTol are twice
-// the bounds (two values are compared), padded.
+// Bounds (the fp32 score of one expert against the real one, in units of 2^-24;
+// ex2.approx is within 2^-22 relative, rcp.approx within 2^-23, and the rounded
+// product l log2(e) moves the exponent by at most 1.5 |l|):
+//   sigmoid  s (1 - s) (4 + 1.5 |l|) + 3 s <= 1 + 0.34 + 3, as s (1 - s) |l| <=
+//            0.224 (3: the sum 1 + exp and the reciprocal);
+//   softmax  p = exp(l - m) / Z, relative to the largest p, x = |l - m|: difference,
+//            product, ex2 and the two roundings of 1 / Z give exp(-x) (6 + 2.5 x)
+//            <= 6; Z sums its terms' relative errors, weighted by the terms,
+//            4 + 2.5 * 7 (the mean of x under p is at most ln 1024 = 7), and NQ + 5
+//            roundings (a lane's NQ terms, then the lanes).
+// The sum v = s + b rounds by |v|.  The tolerances are twice the bounds (two
+// values are compared), rounded up.
 #pragma once
 
 #include <float.h>
@@ -32,9 +31,9 @@
 
 namespace strata {
 
-constexpr float kSigmoidTol = 1e-6f;
-constexpr float kSoftmaxTol = 1.4e-5f;
-constexpr float kSumTol = 1.5e-7f;  // of |v|: two roundings of 2^-24, padded
+constexpr float kSigmoidTol = 9 * 0x1p-24f;
+constexpr float softmax_tol(int nq) { return (66 + 2 * nq) * 0x1p-24f; }
+constexpr float kSumTol = 2.5f * 0x1p-24f;  // of |v|
 
 // One token's logits.
 struct LogitRow {
@@ -398,7 +397,7 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
     const bool odd = rank_values<S, NQ, kSoftmax, kBias, false>(p, row, vec, sl, bias + r, v, m, inv_z, kBias || group_scores);
     if (__any_sync(kAll, odd))
         rank_values<S, NQ, kSoftmax, kBias, true>(p, row, vec, sl, bias + r, v, m, inv_z, kBias || group_scores);
-    const float score_tol = kSoftmax ? kSoftmaxTol * inv_z : kSigmoidTol;
+    const float score_tol = kSoftmax ? softmax_tol(NQ) * inv_z : kSigmoidTol;
 
     // groups, and the lane's best (two) values
     float b1 = -INFINITY, b2 = -INFINITY;
