@@ -373,7 +373,8 @@ enum {
                                    2 force the prefill GEMM, 3 force the fused decode kernel
                                    (T <= 64, E <= 512, k <= 16, H and I multiples of 128, and
                                    its shared-memory plan must give every compute group a ring
-                                   slot; auto mode takes the chain for shapes that do not fit,
+                                   slot, and a routing rule's groups leave a lane at most 16
+                                   experts; auto mode takes the chain for shapes that do not fit,
                                    a forced forward fails with STRATA_ERR_INVALID_ARG) */
     STRATA_OPT_WAIT_BUDGET = 2, /* bound of every device-side wait, in SM clock cycles
                                    (default 4e9); 0 makes every wait give up at once */
