@@ -225,7 +225,8 @@ enum { STRATA_Q8_E4M3 = 0, STRATA_Q8_INT8 = 1 };
  *   y = h r weight (fp32);  xn = bf16(y);  (q, scale) = 8-bit row of y
  *   x_dev      bf16 [T][H]
  *   delta_dev  bf16 [T][H] or NULL (then h = x)
- *   weight_dev [H], bf16 or float as weight_type says, or NULL (then 1)
+ *   weight_dev [H], bf16 or float as weight_type says, magnitudes below 2^96,
+ *              or NULL (then 1)
  *   h_out_dev  bf16 [T][H] out, may be x_dev itself; needed with delta_dev,
  *              may be NULL without
  *   xn_dev     bf16 [T][H] out or NULL

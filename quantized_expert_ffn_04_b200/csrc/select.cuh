@@ -428,18 +428,24 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
             s2 = two ? fast_score<kSoftmax>(t2, m, inv_z, den) : -INFINITY;
         }
         const float gv = two ? s1 + s2 : s1;
-        // two groups closer than this (either's bound) are compared in 64 bits
-        const float near = 2.0f * score_tol + 4.0f * kSumTol * (fabsf(s1) + (two ? fabsf(s2) : 0.0f));
+        // how many groups are ahead: a larger value, or the same and a lower id
+        const uint32_t key = ordered(gv + 0.0f), lower = (1u << g) - 1u;
         int ahead = 0;
-        bool close = false;
 #pragma unroll 4
-        for (int o = 0; o < p.n_groups; o++) {
-            const float other = __shfl_sync(kAll, gv, o << ll, S);
-            ahead += other > gv || (other == gv && o < g);
-            close |= o != g && !(fabsf(other - gv) > near);
-        }
+        for (int o = 0; o < p.n_groups; o++)
+            ahead += __shfl_sync(kAll, key, o << ll, S) + ((lower >> o) & 1u) > key;
         kept = mine && ahead < p.top_groups;
-        const unsigned near64 = kBias || p.sum2 ? __ballot_sync(kAll, close && gv > -INFINITY && mine) : 0u;
+        unsigned near64 = 0;
+        if (kBias || p.sum2) {
+            // the last group that stays and the first that goes: closer than any
+            // two groups' bounds, and 64 bits decide
+            const float size = gv > -INFINITY && mine ? fabsf(s1) + (two ? fabsf(s2) : 0.0f) : 0.0f;
+            const float near = 2.0f * score_tol + 4.0f * kSumTol * lanes_max<S>(size);
+            const int last = __ffs(__ballot_sync(kAll, mine && ahead == p.top_groups - 1) >> base & kSub) - 1;
+            const int next = __ffs(__ballot_sync(kAll, mine && ahead == p.top_groups) >> base & kSub) - 1;
+            const float low = __shfl_sync(kAll, gv, last, S), high = __shfl_sync(kAll, gv, next, S);
+            near64 = __ballot_sync(kAll, high > -INFINITY && !(low - high > near));
+        }
         if (near64) {
             const double none = -(double)INFINITY, iz = token_inv_sum64<S, kSoftmax>(p, row, lane, m, near64);
             double d1 = none, d2 = none;
