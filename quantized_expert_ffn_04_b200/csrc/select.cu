@@ -4,7 +4,7 @@
 // One warp per token here, several tokens a warp in select_batch.cu (select.cuh).
 // The work is one read of the logits and a few hundred instructions a token; the
 // instructions bound it: 65536 tokens of 256 experts (8 groups, sigmoid scores
-// with a bias) take 39 us, 479 instructions a token at 66 % of the issue slots,
+// with a bias) take 39 us, about 470 instructions a token at 66 % of the issue slots,
 // where the read alone would take 11; without groups and bias 23 us.
 #include <math.h>
 
