@@ -79,6 +79,7 @@ __device__ __forceinline__ void join_two(V u1, V u2, V &t1, V &t2) {
 static __device__ __noinline__ double inv_sum64(const SelectPlan &p, LogitRow row, int lane, float m) {
     if (p.score == STRATA_SCORE_SIGMOID) return 1.0;
     double z = 0.0;
+#pragma unroll 4
     for (int e = lane; e < p.E; e += 32) z += exp((double)row.at(e) - (double)m);
     for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     return 1.0 / z;
@@ -342,6 +343,17 @@ __device__ __forceinline__ bool rank_values(const SelectPlan &p, LogitRow row, b
     return !(fabsf(check) < INFINITY);
 }
 
+// Softmax values x >= y with a bias that the tolerance of any two values could
+// not tell apart: the bound of these two.  Z's error, most of the tolerance, is
+// common to both scores, so only their difference carries it; the rest of a
+// score's error is p (6 + 2.5 x) <= 6 p + 0.92 pmax.
+template <int NQ>
+__device__ __forceinline__ bool softmax_pair_close(float x, float y, float bx, float by, float pmax) {
+    const float px = x - bx, py = y - by;
+    const float units = 6.0f * (px + py) + 2.0f * pmax + (30.0f + NQ) * fabsf(px - py);
+    return !(x - y > units * 0x1.1p-24f + 2.0f * kSumTol * fmaxf(fabsf(x), fmaxf(fabsf(bx), fabsf(by))));
+}
+
 // Softmax: 1 / sum in 64 bits of the lane's token, for the tokens with a bit in
 // `which`.
 template <int S, bool kSoftmax>
@@ -380,7 +392,7 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
                                               SelectScratch<S> &scratch, int32_t *idx, float *w,
                                               bool cg = false) {
     constexpr int kCap = SelectScratch<S>::kCap, kOwn = kCap / S;
-    constexpr bool kTwo = S < 32;  // the threshold from every lane's best two
+    constexpr bool kTwo = S < 32;  // the threshold from every lane's second best
     constexpr unsigned kAll = 0xffffffffu, kSub = S == 32 ? kAll : (1u << (S & 31)) - 1u;
     const int lane = threadIdx.x & 31, r = lane % S, base = lane - r;
     const long long t = t0 + lane / S < T ? t0 + lane / S : T - 1;
@@ -481,10 +493,12 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
         }
     }
 
-    // tau: a value that at least k experts reach.  One of the lanes' best (S ==
-    // 32): the k-th largest; two of them: the ceil(k / 2)-th largest of their
-    // second best, as each of those lanes holds two.  -inf when that is too few.
-    float tau = kTwo ? b2 : b1;
+    // tau: a value that at least k experts reach.  Of the lanes' best, the k-th
+    // largest; or, where the batch or the groups leave fewer lanes than picks, the
+    // ceil(k / 2)-th largest of their second best, as each of those lanes holds two.
+    // -inf when that is too few.
+    const bool second = kTwo || (grouped && (p.top_groups << ll) < p.k);
+    float tau = second ? b2 : b1;
 #pragma unroll
     for (int size = 2; size <= S; size <<= 1)  // sorted over the lanes, largest first
 #pragma unroll
@@ -492,7 +506,7 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
             const float x = __shfl_xor_sync(kAll, tau, o);
             tau = ((r & size) == 0) == ((r & o) == 0) ? fmaxf(tau, x) : fminf(tau, x);
         }
-    tau = __shfl_sync(kAll, tau, kTwo ? (p.k - 1) >> 1 : p.k - 1, S);
+    tau = __shfl_sync(kAll, tau, second ? (p.k - 1) >> 1 : p.k - 1, S);
     const float tol = kBias ? score_tol : 0.0f, sum_tol = kBias ? kSumTol : 0.0f;
     auto reach = [&](float x) { return fabsf(x) < INFINITY ? x - (tol + sum_tol * fabsf(x)) : -FLT_MAX; };
     auto count = [&](float x) {
@@ -572,8 +586,11 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
             // neighbours closer than the bound, the first that is left out included
             bool close = false;
             for (int a = r; a < p.k; a += S) {
-                const float x = key_value(sorted[a < n ? a : 0]), y = key_value(sorted[a + 1 < n ? a + 1 : 0]);
-                close |= a + 1 < n && !(x - y > tol + sum_tol * fabsf(x));
+                if (a + 1 >= n) continue;
+                const float x = key_value(sorted[a]), y = key_value(sorted[a + 1]);
+                if (x - y > tol + sum_tol * fabsf(x)) continue;
+                close = close || !kSoftmax ||
+                        softmax_pair_close<NQ>(x, y, p.bias[key_expert(sorted[a])], p.bias[key_expert(sorted[a + 1])], inv_z);
             }
             const unsigned near64 = __ballot_sync(kAll, close);
             if (near64) {
@@ -667,10 +684,11 @@ template <int S>
 constexpr int kSelectWarps = S == 32 ? 4 : 8;
 // Blocks an SM holds at least (a bound on registers).  Batches: 64 registers
 // (65536 tokens of 256 experts, 16 lanes each: 39 us, 46 without the bound).  A
-// token a warp: 72 (8192 tokens of 512: 10.2 us against 11.7), but not where
-// softmax values with a bias would spill (1037 tokens of 160: 6.1 us against 7.4).
+// token a warp: 72 (8192 tokens of 512: 10.2 us against 11.7); softmax values with
+// a bias, which would spill there, 96 (1037 tokens of 512: 4.8 us, 5.9 with 72;
+// 8192: 11.6, 13.6 without the bound).
 template <int S, int NQ, bool kSpills>
-constexpr int kSelectBlocks = S < 32 ? 4 : NQ > 32 ? 2 : NQ > 16 || kSpills ? 4 : 7;
+constexpr int kSelectBlocks = S < 32 ? 4 : NQ > 32 ? 2 : NQ > 16 ? 4 : kSpills ? 5 : 7;
 
 template <int S, int NQ, bool kSoftmax, bool kBias>
 __global__ __launch_bounds__(32 * kSelectWarps<S>, kSelectBlocks<S, NQ, kSoftmax && kBias>) void route_logits_kernel(

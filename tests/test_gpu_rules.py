@@ -83,7 +83,8 @@ def test_rules_match_the_plain_form(rule, groups, bias):
 
 @pytest.mark.parametrize("E,k,n,top", [(1, 1, 1, 1), (2, 2, 1, 1), (3, 2, 1, 1), (31, 31, 1, 1), (33, 32, 1, 1), (32, 32, 1, 1),
                                        (1020, 32, 17, 3), (1024, 32, 32, 1), (990, 7, 30, 2), (62, 4, 31, 2), (64, 2, 32, 1),
-                                       (1023, 32, 1, 1), (1024, 32, 1, 1), (513, 9, 3, 1), (96, 32, 3, 2)])
+                                       (1023, 32, 1, 1), (1024, 32, 1, 1), (513, 9, 3, 1), (96, 32, 3, 2),
+                                       (16, 4, 16, 5), (32, 7, 32, 9), (32, 16, 4, 2), (128, 32, 4, 1)])
 def test_odd_sizes(E, k, n, top):
     for score in ("softmax", "sigmoid"):
         for bias in (None, bias_of(E, E)):
@@ -228,6 +229,28 @@ def test_near_ties_are_decided_in_64_bits():
     for kw in [dict(score="sigmoid"), dict(score="softmax"), dict(score="softmax", n_groups=4, top_groups=2, group_score="sum2")]:
         check(l2, 9, np.full(E, 0.125, np.float32), **kw)
         check(l2, 9, None, **kw)
+
+
+def test_softmax_pairs_that_only_their_own_bound_tells_apart():
+    """Softmax values a few units of 2^-24 apart: with equal biases (the sum's
+    error is common and tells nothing), with biases that cancel the scores, with
+    large biases."""
+    rng = np.random.default_rng(33)
+    T, E = 400, 64
+    l = logits_of(T, E, 34, 1.0)
+    top = np.argsort(-l, 1)[:, :2]
+    rows = np.arange(T)
+    for ulps in (1, 2, 5, 20):  # the two largest logits of a row, some units apart
+        x = l.copy()
+        x[rows, top[:, 1]] = x[rows, top[:, 0]] * (1 - ulps * np.float32(2.0 ** -23))
+        check(x, 8, np.zeros(E, np.float32))
+        check(x, 8, np.full(E, 3.0, np.float32))
+        check(x, 8, (1e-7 * rng.standard_normal(E)).astype(np.float32), renorm=False)
+    p = np.exp(l[0].astype(np.float64) - l[0].max())
+    p /= p.sum()
+    b = (0.25 - p + 1e-9 * rng.standard_normal(E)).astype(np.float32)  # row 0: all values near 1/4
+    check(l, 8, b)
+    check(np.tile(l[:1], (9000, 1)) + 1e-6 * rng.standard_normal((9000, 1)).astype(np.float32), 8, b)
 
 
 def test_bias_cancels_the_score():
