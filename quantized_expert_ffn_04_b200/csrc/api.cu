@@ -479,6 +479,7 @@ strata_status strata::refuse(const char *who, const char *what) {
 
 strata_status strata::launched(const char *who, cudaError_t e) {
     if (e == cudaSuccess) return STRATA_OK;
+    cudaGetLastError();  // reported here, not by a later call
     return fail(STRATA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
 }
 

@@ -291,6 +291,25 @@ def test_dequant_rows_exactly(n, src, H, group, q8):
         assert ((out[:n] == ref) | (torch.isnan(out[:n]) & torch.isnan(ref))).all()
 
 
+@pytest.mark.parametrize("q8", ["e4m3", "int8"])
+def test_dequant_to_rows_on_16_bytes_only(q8):
+    """An output that starts between two 32-byte lines."""
+    rng = np.random.default_rng(4)
+    H, n = 96, 37
+    code = all_codes(q8, n, H, rng)
+    scale = torch.from_numpy(np.exp(rng.standard_normal((n, 3))).astype(np.float32)).cuda()
+    buf = torch.full((n * H + 24,), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert buf.data_ptr() % 32 == 0
+    for off in (0, 8):
+        buf.fill_(7.0)
+        out = buf[off:off + n * H].view(n, H)
+        qe.strata_moe_dequant_rows(code.data_ptr(), Q8[q8][0], H, scale.data_ptr(), 3, 32, None, n, n, H, out.data_ptr())
+        torch.cuda.synchronize()
+        ref = (code.view(Q8[q8][1]).float() * scale.repeat_interleave(32, 1)).to(torch.bfloat16)
+        assert ((out == ref) | (torch.isnan(out) & torch.isnan(ref))).all()
+        assert (buf[:off] == 7.0).all() and (buf[off + n * H:] == 7.0).all()
+
+
 def test_offsets_past_32_bits():
     """Rows further than 2^32 bytes into the codes and the output."""
     H, group = 65536, 0
