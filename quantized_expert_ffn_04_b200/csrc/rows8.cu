@@ -85,6 +85,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return m;
 }
 
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 // Sum over the row's 32-vector blocks: v[i] is this thread's part of block
 // i * warps + warp.  A tree inside each block, then one over the blocks, so the
 // sum does not depend on how many vectors a thread holds.
@@ -149,10 +152,14 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_
         for (int q = 0; q < 8; q++) part[i] = fmaf(h[i][q], h[i][q], part[i]);
     }
     const float ss = row_sum<NV>(part, fs);
-    // r = 1 / sqrt(mean + eps).  Where the squares' sum comes near the ends of
-    // fp32's range: in 64 bits, and r = unit * rr with unit a power of two that
-    // h is multiplied by first
+    // r = 1 / sqrt(mean + eps), in 64 bits where the squares' sum comes near the
+    // ends of fp32's range.  A factor above 2 is split: its power of two goes into
+    // h, exactly (|h| r <= sqrt(H)), and r stays in [1, 2).  So t = h w below is
+    // within a factor of 2 of y = t r (or above it), and leaves fp32's normal range
+    // only where y does.
     float r = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(ss, a.inv_h, a.eps)));
+    float late = 1.0f;  // below 1: the power of two of a small r, see times_late
+    int ex = 0;
     if ((ss < 0x1p-60f && a.eps < 0x1p-60f) || !(ss < 0x1p60f)) {
         double dp[NV];
 #pragma unroll
@@ -162,18 +169,31 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_
             for (int q = 0; q < 8; q++) dp[i] = fma((double)h[i][q], (double)h[i][q], dp[i]);
         }
         const double rd = 1.0 / sqrt(row_sum<NV>(dp, ds) / a.H + (double)a.eps);
-        const int ex = rd > 0.0 && rd < INFINITY ? max(-126, min(126, ilogb(rd))) : 0;
-        const float unit = __uint_as_float((uint32_t)(127 + ex) << 23);
-        r = (float)(rd / (double)unit);
+        ex = rd > 0.0 && rd < INFINITY ? max(-126, ilogb(rd)) : 0;  // at most 140
+        r = (float)scalbn(rd, -ex);
+        if (ex < 0) late = pow2(ex);
+    } else if (r >= 2.0f) {
+        ex = (int)(__float_as_uint(r) >> 23) - 127;
+        r *= pow2(-ex);
+    }
+    if (ex > 0) {
+        const float up = pow2(min(ex, 126)), rest = pow2(max(ex, 126) - 126);
 #pragma unroll
         for (int i = 0; i < NV; i++)
 #pragma unroll
-            for (int q = 0; q < 8; q++) h[i][q] *= unit;
+            for (int q = 0; q < 8; q++) h[i][q] = h[i][q] * up * rest;
     }
+    // h w 2^ex for ex < 0: the power first where h is large (h w might overflow), last
+    // where it is not (h 2^ex might underflow)
+    auto times_late = [&](float v, float w) {
+        const bool first = fabsf(v) >= 1.0f;
+        return v * (first ? late : 1.0f) * w * (first ? 1.0f : late);
+    };
     constexpr float kMax = kQ8 == STRATA_Q8_E4M3 ? kE4m3Max : kInt8Max;
     // y = t r with t = h w (exact for bf16 weights).  A code is the rounded
     // quotient kMax t / max|t|: (c t) / m with m = max|t| scaled into [1, 2) and c
-    // = kMax times the same power of two, both exact where t is.  The quotient is
+    // = kMax times the same power of two, both exact where t is (y >= 2^-116 and r <=
+    // 2 leave max|t| >= 2^-117, so c <= 448 2^117).  The quotient is
     // corrected once by its remainder (Markstein's method), which makes it exact
     // where it is representable: a value exactly between two codes goes to the
     // even one, as it does in 64 bits.
@@ -210,8 +230,10 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int c = i * threads + tid;
+        float w[8];
+#pragma unroll
+        for (int q = 0; q < 8; q++) w[q] = 1.0f;
         if (a.weight && c < nv) {
-            float w[8];
             if (kF32Weight) {
                 const float4 u = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * c);
                 const float4 v = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * c + 1);
@@ -219,8 +241,13 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_
             } else {
                 unpack8(__ldg(reinterpret_cast<const uint4 *>(a.weight) + c), w);
             }
+        }
+        if (late == 1.0f) {
 #pragma unroll
             for (int q = 0; q < 8; q++) h[i][q] *= w[q];
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; q++) h[i][q] = times_late(h[i][q], w[q]);
         }
         if (a.xn && c < nv) {
             float o[8];

@@ -355,3 +355,62 @@ def test_streams_and_graph():
         g.replay()
     torch.cuda.synchronize()
     n.check(f64(x2), f64(d2), f64(w))
+
+
+def range_rows(H, rng):
+    """Rows whose norm's factor runs from 2^-127 to 2^70, and rows with parts far
+    below their mean, where another part's squares decide the factor."""
+    z = rng.standard_normal((16, H))
+    level = np.exp2([2, 0, -3, -6, -10, -20, -29, -31, -60, -70, 29, 31, 64, 100, 123, 0])
+    x = np.clip(z, -5, 5) * level[:, None]
+    part = np.arange(H) // 128
+    for row in (10, 13, 14):
+        for p in range(8):  # from the row's own level down to 2^-140 of it
+            x[row, part == p] *= np.exp2(-20.0 * p)
+    x[15, 128:] *= 2.0 ** -40
+    return bf16(x)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("wt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("q8", ["e4m3", "int8"])
+def test_rows_over_the_whole_range(q8, group, wt, eps):
+    """bf16 rows, codes and scales of rows of any size under weights of any size:
+    products of a row's value and a weight that leave fp32's normal range on
+    either side while their normalised value is well inside it."""
+    H = 1024
+    rng = np.random.default_rng(97)
+    x = range_rows(H, rng)
+    T = x.shape[0]
+    sizes = np.array([[1.0, 1e-34, 1.5e-36, 2.0 ** -115, 2.0 ** -119, 1e-38, 3e-40, 1.0],  # the last three: no codes
+                      [2.0 ** 95] * 8, [1e-34] * 8, [2.0 ** -112] * 8, [1.0, 2.0 ** 95, 1e-30, 2.0 ** 60, 1e-20, 2.0 ** 90, 1e-3, 1e-36]])
+    for size in sizes:
+        w = (np.repeat(size, 128) * rng.uniform(0.5, 1.0, H)).astype(np.float32)
+        w = torch.from_numpy(w).cuda().to(wt)
+        n = Norm(x, None, w, eps=eps, q8=q8, group=group)
+        n.go()
+        torch.cuda.synchronize()
+        _, y = norm_rows(f64(x), None, f64(w), eps)
+        # below the normal range fp32 and bf16 round by half their smallest steps, 2^-150 (twice) and 2^-134
+        err = np.abs(f64(n.xn[:T]) - y)
+        assert (err <= (2.0 ** -8 + FP32_TOL) * np.abs(y) + 2.0 ** -134 + 2.0 ** -149).all()
+        top = Q8[q8][2]
+        big = np.abs(y).reshape(T, n.ns, -1).max(2)
+        c, s = n.codes()
+        c, s = c.reshape(T, n.ns, -1), s.reshape(T, n.ns, -1)[:, :, 0]
+        none, some = big < 2.0 ** -116 * (1 - FP32_TOL), big > 2.0 ** -116 * (1 + FP32_TOL)
+        assert (s[none] == 0).all() and (c[none] == 0).all()
+        np.testing.assert_allclose(s[some], big[some] / top, rtol=FP32_TOL)
+        assert (np.abs(c).max(2)[some] == top).all()
+        e, s = np.abs(c * s[:, :, None] - y.reshape(c.shape))[some], s[some][:, None]
+        if q8 == "e4m3":
+            assert (e <= (2.0 ** -4 + 3 * FP32_TOL) * np.abs(y.reshape(c.shape)[some]) + s * (2.0 ** -10 + 1e-9)).all()
+        else:
+            assert (e <= s * (0.5 + 2 * 127 * FP32_TOL)).all()
+    # without a weight
+    n = Norm(x, None, None, eps=eps)
+    n.go()
+    torch.cuda.synchronize()
+    _, y = norm_rows(f64(x), None, None, eps)
+    assert (np.abs(f64(n.xn[:T]) - y) <= (2.0 ** -8 + FP32_TOL) * np.abs(y) + 2.0 ** -134 + 2.0 ** -149).all()
