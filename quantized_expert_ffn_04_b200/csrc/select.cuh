@@ -583,14 +583,16 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
         }
         __syncwarp();
         if (kBias) {
-            // neighbours closer than the bound, the first that is left out included
+            // neighbours closer than the bound: of the picks, and of the last pick with
+            // those left out.  Softmax pairs have bounds of their own, which a value
+            // further behind may exceed where the next one does not, so the last pick
+            // is compared with every one that the common bound reaches.
             bool close = false;
-            for (int a = r; a < p.k; a += S) {
-                if (a + 1 >= n) continue;
-                const float x = key_value(sorted[a]), y = key_value(sorted[a + 1]);
+            for (int a = r; a + 1 < n && (kSoftmax || a < p.k); a += S) {
+                const unsigned long long kx = sorted[min(a, p.k - 1)], ky = sorted[a + 1];
+                const float x = key_value(kx), y = key_value(ky);
                 if (x - y > tol + sum_tol * fabsf(x)) continue;
-                close = close || !kSoftmax ||
-                        softmax_pair_close<NQ>(x, y, p.bias[key_expert(sorted[a])], p.bias[key_expert(sorted[a + 1])], inv_z);
+                close = close || !kSoftmax || softmax_pair_close<NQ>(x, y, p.bias[key_expert(kx)], p.bias[key_expert(ky)], inv_z);
             }
             const unsigned near64 = __ballot_sync(kAll, close);
             if (near64) {

@@ -513,3 +513,52 @@ def test_set_routing_keeps_the_old_rule_when_refused_and_counts_launches():
     qe.strata_moe_debug_fail_alloc(-1)
     assert e.value.status == qe.STRATA_ERR_OOM
     L.close()
+
+
+def triples(T, E, share, unit_gap, seed):
+    """Rows and a bias with three values next to each other: experts 7 and 11 with
+    scores near 0, `unit_gap` units of 2^-24 of the largest score apart, and
+    expert 3, the row's most likely one (score about `share`) with a bias that
+    cancels it, whose value lies above both by less than half a unit."""
+    rng = np.random.default_rng(seed)
+    unit = share * 2.0 ** -24
+    l = rng.standard_normal((T, E))
+    l[:, [7, 11]] = -200
+    rest = np.delete(np.arange(E), [3, 7, 11])
+    odds = np.exp(0.35) * (1 - share) / share  # sum of the others' exp for a logit of 0.35
+    l[:, rest] += np.log(odds) - np.log(np.exp(l[:, rest]).sum(1, keepdims=True))
+    l = l.astype(np.float32)
+    l = np.minimum(l, np.float32(0.2))
+    bias = np.full(E, -4.0, np.float32)
+    low = np.float32(2.0 ** -9)
+    bias[3] = np.float32(low - share)
+    bias[7] = low
+    bias[11] = np.float32(low - unit_gap * unit)
+    others = l.astype(np.float64)
+    others[:, 3] = -np.inf
+    s = np.exp(others).sum(1)
+    want = np.float64(low) - np.float64(bias[3]) + 0.02 * unit  # expert 3's score
+    l[:, 3] = np.log(want * s / (1 - want))
+    p = lambda: np.exp(l[:, 3].astype(np.float64)) / (s + np.exp(l[:, 3].astype(np.float64)))  # noqa: E731
+    for _ in range(3):  # the first float at or above it
+        under = p() < want
+        l[under, 3] = np.nextafter(l[under, 3], np.float32(np.inf))
+    ok = (p() >= want) & (p() - want < 0.4 * unit) & (l[:, 3] > l[:, rest].max(1))
+    return l[ok], bias
+
+
+@pytest.mark.parametrize("E,share", [(512, 0.4), (1024, 0.3), (512, 0.2), (160, 0.4)])
+def test_softmax_values_behind_the_first_one_left_out(E, share):
+    """A value that lies two places behind the last pick in fp32 and is the pick
+    in 64 bits: its score's error is larger than that of the two before it."""
+    for gap in (2.14, 2.2, 2.5, 3.0):
+        l, bias = triples(20000, E, share, gap, E)
+        T = l.shape[0]
+        assert T > 8192
+        for n in (T, 8191):  # several tokens a warp, and one
+            idx, _ = call(l[:n], 1, bias)
+            assert (idx == 3).all(), (n, gap, (idx != 3).sum())
+            idx, _ = call(l[:n], 2, bias)
+            assert (idx == [3, 7]).all(), (n, gap, (idx != [3, 7]).any(1).sum())
+            idx, _ = call(l[:n], 3, bias)
+            assert (idx == [3, 7, 11]).all(), (n, gap)
