@@ -439,7 +439,8 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
             s1 = t1 > -INFINITY ? fast_score<kSoftmax>(t1, m, inv_z, den) : -INFINITY;
             s2 = two ? fast_score<kSoftmax>(t2, m, inv_z, den) : -INFINITY;
         }
-        const float gv = two ? s1 + s2 : s1;
+        // (without a bias a best value is the logit, +inf the largest finite float)
+        const float gv = two ? s1 + s2 : kBias ? s1 : fminf(s1, FLT_MAX);
         // how many groups are ahead: a larger value, or the same and a lower id
         const uint32_t key = ordered(gv + 0.0f), lower = (1u << g) - 1u;
         int ahead = 0;

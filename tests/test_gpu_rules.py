@@ -562,3 +562,25 @@ def test_softmax_values_behind_the_first_one_left_out(E, share):
             assert (idx == [3, 7]).all(), (n, gap, (idx != [3, 7]).any(1).sum())
             idx, _ = call(l[:n], 3, bias)
             assert (idx == [3, 7, 11]).all(), (n, gap)
+
+
+@pytest.mark.parametrize("T", [1, 9001, 17001])
+def test_infinite_and_largest_logits_tie_between_groups(T):
+    """+inf counts as the largest finite float in the choice of groups as well: a
+    tie there goes to the lower group."""
+    E, big = 64, np.finfo(np.float32).max
+    l = logits_of(T, E, 80)
+    l[::2, 10] = big            # group 1 of 8
+    l[::2, 45] = np.inf         # group 5
+    l[1::2, 3] = np.inf
+    l[1::2, 60] = big
+    sample = np.unique(np.r_[0:min(T, 40), max(0, T - 40):T])
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            for top in (1, 2):
+                for gsc in ("best", "sum2"):
+                    kw = dict(score=score, renorm=renorm, n_groups=8, top_groups=top, group_score=gsc)
+                    idx, w = call(l, 3, None, **kw)
+                    ridx, rw = route_rule(l[sample], 3, **kw)
+                    assert np.array_equal(idx[sample], ridx), kw
+                    np.testing.assert_allclose(w[sample], rw, rtol=W_TOL_PLAIN_SOFTMAX, atol=1e-37)
