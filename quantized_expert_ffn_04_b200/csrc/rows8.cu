@@ -230,10 +230,8 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         const int c = i * threads + tid;
-        float w[8];
-#pragma unroll
-        for (int q = 0; q < 8; q++) w[q] = 1.0f;
         if (a.weight && c < nv) {
+            float w[8];
             if (kF32Weight) {
                 const float4 u = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * c);
                 const float4 v = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * c + 1);
@@ -241,13 +239,16 @@ __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_
             } else {
                 unpack8(__ldg(reinterpret_cast<const uint4 *>(a.weight) + c), w);
             }
-        }
-        if (late == 1.0f) {
+            if (late == 1.0f) {
 #pragma unroll
-            for (int q = 0; q < 8; q++) h[i][q] *= w[q];
-        } else {
+                for (int q = 0; q < 8; q++) h[i][q] *= w[q];
+            } else {
 #pragma unroll
-            for (int q = 0; q < 8; q++) h[i][q] = times_late(h[i][q], w[q]);
+                for (int q = 0; q < 8; q++) h[i][q] = times_late(h[i][q], w[q]);
+            }
+        } else if (late < 1.0f) {
+#pragma unroll
+            for (int q = 0; q < 8; q++) h[i][q] *= late;
         }
         if (a.xn && c < nv) {
             float o[8];
