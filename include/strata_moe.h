@@ -154,7 +154,10 @@ strata_status strata_moe_forward(strata_moe_t h, const void *x_dev, int T, void 
  * of -inf or NaN, or a bias of -inf or NaN, is not eligible: it adds nothing
  * to its group, and where fewer than k eligible experts stay, the other picks
  * are the lowest remaining ids with weight 0 (so picks are always k different
- * valid ids).  A logit of +inf counts as the largest finite float. */
+ * valid ids).  A logit of +inf counts as the largest finite float.
+ * A token's picks follow from its own logits alone.  So do its weights in a call
+ * of the same T; with another T their last bits may differ, as fewer or more
+ * lanes then sum a token's scores. */
 enum { STRATA_SCORE_SOFTMAX = 0, STRATA_SCORE_SIGMOID = 1 };
 enum { STRATA_GROUP_BEST = 0, STRATA_GROUP_SUM2 = 1 };
 /* Element types of caller buffers that may have either. */

@@ -623,7 +623,8 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
             }
         }
         // picks r, r + S, ... and their weights, of which the sum is taken
-        // relative to the largest pick where it would leave fp32's normal range
+        // relative to the largest pick where it would leave fp32's normal range (for
+        // that token alone: a token's weights do not depend on the warp's others)
         constexpr int kPicks = S < 32 ? 16 / S : 1;  // k <= 16 there
         float l[kPicks], s[kPicks], sum = 0.0f;
         int e[kPicks];
@@ -644,7 +645,8 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
         float f = p.scale;
         if (p.renorm) {
             sum = lanes_sum<S>(sum);
-            if (__any_sync(kAll, sum < 0x1p-60f && n)) {
+            const bool tiny = sum < 0x1p-60f && n;
+            if (__any_sync(kAll, tiny)) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < kPicks; q++) top = r + q * S < p.k ? fmaxf(top, l[q]) : top;
@@ -653,7 +655,7 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
                 sum = 0.0f;
 #pragma unroll
                 for (int q = 0; q < kPicks; q++) {
-                    if (r + q * S < p.k && n) s[q] = pick_score<kSoftmax>(l[q], top, 1.0f);
+                    if (r + q * S < p.k && tiny) s[q] = pick_score<kSoftmax>(l[q], top, 1.0f);
                     sum += s[q];
                 }
                 sum = lanes_sum<S>(sum);

@@ -584,3 +584,27 @@ def test_infinite_and_largest_logits_tie_between_groups(T):
                     ridx, rw = route_rule(l[sample], 3, **kw)
                     assert np.array_equal(idx[sample], ridx), kw
                     np.testing.assert_allclose(w[sample], rw, rtol=W_TOL_PLAIN_SOFTMAX, atol=1e-37)
+
+
+@pytest.mark.parametrize("E", [64, 256])
+def test_a_token_s_weights_do_not_depend_on_its_neighbours(E):
+    """Tokens with scores near fp32's smallest next to ordinary ones, several
+    tokens a warp: the ordinary ones keep their bits."""
+    k = 6
+    for T in (9001, 17001):
+        l = logits_of(T, E, 90)
+        odd = l.copy()
+        odd[::3] -= 95
+        for score in ("sigmoid", "softmax"):
+            for bias in (None, bias_of(E, 8, 0.2 / E)):
+                for renorm in (True, False):
+                    kw = dict(score=score, renorm=renorm)
+                    if score == "softmax" and bias is not None:
+                        # one expert takes all, and the bias picks others
+                        odd = l.copy()
+                        odd[::3, 5] += 120
+                        bias[5] = -2
+                    idx, w = call(l, k, bias, **kw)
+                    i2, w2 = call(odd, k, bias, **kw)
+                    keep = np.arange(T) % 3 != 0
+                    assert np.array_equal(idx[keep], i2[keep]) and np.array_equal(w[keep], w2[keep]), kw
