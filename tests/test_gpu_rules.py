@@ -608,3 +608,28 @@ def test_a_token_s_weights_do_not_depend_on_its_neighbours(E):
                     i2, w2 = call(odd, k, bias, **kw)
                     keep = np.arange(T) % 3 != 0
                     assert np.array_equal(idx[keep], i2[keep]) and np.array_equal(w[keep], w2[keep]), kw
+
+
+@pytest.mark.parametrize("T", [16, 9001, 17001])
+def test_extreme_logits_with_a_bias(T):
+    """Scores that underflow, that all round to one, or of which one takes all,
+    where the bias then decides."""
+    E, k = 64, 6
+    rows = logits_of(T, E, 21)
+    for i, t in enumerate((0, 1, 2, 3, 4, 5, 6, T - 2, T - 1)):
+        base = rows[t].copy()
+        rows[t] = [-200 + base, 60 + base, np.float32(1e30) * base, -88.5 + np.float32(0.01) * base, 17 + base, -17 + base,
+                   np.float32(-1e30) * np.abs(base), np.full(E, 5.0), 1e-30 * base][i]
+    sample = np.unique(np.r_[0:14, T - 12:T])
+    sizes = {"large": bias_of(E, 5, 0.05), "equal": np.full(E, 0.25, np.float32), "none": np.zeros(E, np.float32),
+             "tiny": bias_of(E, 6, 1e-9)}
+    for groups in [dict(), dict(n_groups=8, top_groups=2), dict(n_groups=8, top_groups=4, group_score="sum2")]:
+        for score in ("softmax", "sigmoid"):
+            for renorm in (True, False):
+                for name, bias in sizes.items():
+                    kw = dict(score=score, renorm=renorm, **groups)
+                    idx, w = call(rows, k, bias, **kw)
+                    ridx, rw = route_rule(rows[sample], k, bias=bias, **kw)
+                    assert np.array_equal(idx[sample], ridx), (kw, name, sample[np.any(idx[sample] != ridx, axis=1)])
+                    np.testing.assert_allclose(w[sample], rw, rtol=W_TOL if score == "sigmoid" or renorm else W_TOL_PLAIN_SOFTMAX,
+                                               atol=1e-37)
