@@ -143,3 +143,40 @@ def test_tensor_functions_refuse():
     assert e[0].shape == (0, 4)
     h, xn, packed = qe.add_rmsnorm(torch.empty(0, 256, device="cuda", dtype=torch.bfloat16), quant="int8", group=0)
     assert packed.shape == (0, 272) and qe.dequant_rows(packed, 256, "int8", 0).shape == (0, 256)
+
+
+@pytest.mark.parametrize("shape,T", [(gen.TINY, 5), (gen.TINY, 100), (gen.FLASH2, 4)], ids=["tiny-5", "tiny-100", "flash-4"])
+def test_plain_forward_equals_its_steps_on_bf16_rows(one_rank, shape, T):
+    """ExpertParallel.forward sends its rows as they are: bit for bit the same steps
+    without an exchange, and the layer's own output on the same kernels."""
+    k, H = shape.top_k, shape.hidden
+    layer, L, sb = rule_layer(shape, T + T * k, seed=1)
+    x = to_dev_bf16(gen.hidden(T, H, seed=15))
+    sent = []
+
+    class Watched(GpuBackend):
+        def gather_rows(self, src, rows):
+            sent.append((src.dtype, tuple(src.shape)))
+            return super().gather_rows(src, rows)
+
+    y = ExpertParallel(Watched(L), shape.n_experts, k, H).forward(x)
+    L.sync_status()
+    assert sent == [(torch.bfloat16, (T, H))]
+    idx, w, _, _ = L.route(x)
+    prefill = T > 64
+    yd = torch.float16 if prefill else torch.float32
+    rows = torch.cat([x, x.repeat_interleave(k, dim=0)])
+    ids = torch.cat([torch.full((T,), -1, dtype=torch.int32, device="cuda"), idx.reshape(-1)])
+    out = torch.empty((T + T * k, H), dtype=yd, device="cuda")
+    Y = torch.empty((T * k + T, H), dtype=yd, device="cuda")
+    qe.strata_moe_expert_rows(L.handle, rows.data_ptr(), ids.data_ptr(), T + T * k, T, prefill, out.data_ptr(), Y[T * k:].data_ptr())
+    Y[:T * k] = out[T:]
+    slot = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    ref = torch.empty_like(x)
+    qe.strata_moe_combine_rows(L.handle, x.data_ptr(), T, idx.data_ptr(), w.data_ptr(), slot.data_ptr(), Y.data_ptr(), prefill, ref.data_ptr())
+    L.sync_status()
+    assert torch.equal(y, ref)
+    L.set_option(qe.STRATA_OPT_PATH, 2 if prefill else 1)
+    assert torch.equal(y, L.forward(x))
+    L.sync_status()
+    L.close()
