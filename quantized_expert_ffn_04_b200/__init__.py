@@ -3,8 +3,17 @@
 Argument marshalling only: every function forwards to the C entry point of
 the same name declared in include/strata_moe.h, and every step of the layer
 runs in the library's CUDA kernels.  PyTorch is used only for device memory
-and streams in the `Layer` convenience wrapper.  There is no fallback: if the
-shared library has not been built, importing this package raises.
+and streams in the torch-tensor functions and the `Layer` convenience wrapper.
+There is no fallback: if the shared library has not been built, importing this
+package raises.
+
+Streams.  The functions named like C entry points take a raw pointer (None: the
+legacy default stream).  The torch-tensor functions and `Layer` take a torch
+stream; without one they run on torch's current stream of their tensors' device,
+so that they follow what made their inputs and become part of a graph that is
+being captured.  With one, the caller orders it with the streams that make the
+inputs and use the outputs.  A layer has one workspace and serves one call at a
+time: calls of a layer on two streams have to be ordered by the caller.
 """
 from __future__ import annotations
 
@@ -281,6 +290,26 @@ def _rows(t, name, dtypes, cols=None):
     return t.data_ptr()
 
 
+def _stream_ptr(stream, device):
+    """A torch stream's pointer; without one, the device's current stream's."""
+    import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _output(stream, make, *args, **kw):
+    """A tensor that a call on `stream` writes: memory of that stream, not used again
+    before the current stream is done with it either."""
+    import torch
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    current = torch.cuda.current_stream(t.device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
 def _same_device(first, *others):
     for t in others:
         if t is not None and t.device != first.device:
@@ -302,11 +331,11 @@ def route_logits(logits, rule, k, select_bias=None, stream=None):
         if select_bias.dtype != torch.float32 or select_bias.shape != (E,) or not select_bias.is_contiguous():
             raise ValueError(f"select_bias must be a contiguous float32 tensor of {E} values")
         bias = select_bias.data_ptr()
-    idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    idx = _output(stream, torch.empty, (T, k), dtype=torch.int32, device=logits.device)
+    w = _output(stream, torch.empty, (T, k), dtype=torch.float32, device=logits.device)
     strata_moe_route_logits(rule, logits.data_ptr(), STRATA_F32 if logits.dtype == torch.float32 else STRATA_BF16,
                             logits.stride(0) if T > 1 else max(E, 1), bias, T, E, k, idx.data_ptr(), w.data_ptr(),
-                            _stream_ptr(stream))
+                            _stream_ptr(stream, logits.device))
     return idx, w
 
 
@@ -333,20 +362,20 @@ def add_rmsnorm(x, delta=None, weight=None, eps=1e-6, quant=None, group=128, wan
         raise ValueError(f"weight must be a contiguous float32 or bfloat16 tensor of {H} values")
     if quant is not None and quant not in _Q8:
         raise ValueError(f"unknown 8-bit type {quant!r}")
-    h = x if delta is None else torch.empty_like(x)
-    xn = torch.empty_like(x) if want_xn else None
+    h = x if delta is None else _output(stream, torch.empty_like, x)
+    xn = _output(stream, torch.empty_like, x) if want_xn else None
     packed = scale = None
     rb = 0
     if quant is not None:
         rb = packed_row_bytes(H, group)
-        packed = torch.empty((T, rb), dtype=torch.uint8, device=x.device)
+        packed = _output(stream, torch.empty, (T, rb), dtype=torch.uint8, device=x.device)
         scale = packed.data_ptr() + H
     if T:
         strata_moe_add_rmsnorm(xp, dp, None if weight is None else weight.data_ptr(),
                                STRATA_BF16 if weight is not None and weight.dtype == torch.bfloat16 else STRATA_F32,
                                eps, T, H, None if delta is None else h.data_ptr(), None if xn is None else xn.data_ptr(),
                                _Q8[quant] if quant else 0, group, None if packed is None else packed.data_ptr(), rb,
-                               scale, rb // 4, _stream_ptr(stream))
+                               scale, rb // 4, _stream_ptr(stream, x.device))
     return h, xn, packed
 
 
@@ -364,13 +393,13 @@ def dequant_rows(packed, H, quant="e4m3", group=128, rows=None, out=None, stream
         n = rows.shape[0]
     _same_device(packed, rows, out)
     if out is None:
-        out = torch.empty((n, H), dtype=torch.bfloat16, device=packed.device)
+        out = _output(stream, torch.empty, (n, H), dtype=torch.bfloat16, device=packed.device)
     op = _rows(out, "out", (torch.bfloat16,), H)
     if out.shape[0] != n:
         raise ValueError(f"out must have {n} rows")
     rb = packed.shape[1]
     strata_moe_dequant_rows(p, _Q8[quant], rb, p + H, rb // 4, group, None if rows is None else rows.data_ptr(), n,
-                            packed.shape[0], H, op, _stream_ptr(stream))
+                            packed.shape[0], H, op, _stream_ptr(stream, packed.device))
     return out
 
 
@@ -394,10 +423,6 @@ def make_weights(layer) -> tuple[strata_moe_weights, list]:
             np.ascontiguousarray(layer.shared_scales, dtype=np.uint16)]
     ptr = [None if a is None else a.ctypes.data for a in keep]
     return strata_moe_weights(*ptr), keep
-
-
-def _stream_ptr(stream):
-    return None if stream is None else stream.cuda_stream
 
 
 class Layer:
@@ -433,24 +458,24 @@ class Layer:
         import torch
         T = x.shape[0]
         if out is None:
-            out = torch.empty_like(x)
-        strata_moe_forward(self.handle, x.data_ptr(), T, out.data_ptr(), _stream_ptr(stream))
+            out = _output(stream, torch.empty_like, x)
+        strata_moe_forward(self.handle, x.data_ptr(), T, out.data_ptr(), _stream_ptr(stream, x.device))
         return out
 
     def route(self, x, stream=None):
         import torch
         T, k, E = x.shape[0], self.shape.top_k, self.shape.n_experts
         dev = x.device
-        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-        w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        off = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        lst = torch.empty(T * k, dtype=torch.int32, device=dev)
+        idx = _output(stream, torch.empty, (T, k), dtype=torch.int32, device=dev)
+        w = _output(stream, torch.empty, (T, k), dtype=torch.float32, device=dev)
+        off = _output(stream, torch.empty, E + 1, dtype=torch.int32, device=dev)
+        lst = _output(stream, torch.empty, T * k, dtype=torch.int32, device=dev)
         strata_moe_route(self.handle, x.data_ptr(), T, idx.data_ptr(), w.data_ptr(),
-                         off.data_ptr(), lst.data_ptr(), _stream_ptr(stream))
+                         off.data_ptr(), lst.data_ptr(), _stream_ptr(stream, dev))
         return idx, w, off, lst
 
     def sync_status(self, stream=None):
-        strata_moe_sync_status(self.handle, _stream_ptr(stream))
+        strata_moe_sync_status(self.handle, _stream_ptr(stream, self.device))
 
     def debug_dequant(self, expert, mat, row0, nrows, kind=0):
         import numpy as np

@@ -36,8 +36,9 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (Layer, add_rmsnorm, dequant_rows, strata_ep_expert_range, strata_ep_gather_rows,
-               strata_ep_plan, strata_moe_combine_rows, strata_moe_expert_rows)
+from . import (Layer, _stream_ptr, add_rmsnorm, dequant_rows, strata_ep_expert_range,
+               strata_ep_gather_rows, strata_ep_plan, strata_moe_combine_rows,
+               strata_moe_expert_rows)
 
 # decode (the GEMV kernels, fp32 expert outputs) up to this many tokens, like
 # the one-GPU forward's default; the tensor-core kernels (fp16 outputs) above
@@ -48,7 +49,8 @@ EXCHANGE_Q8, EXCHANGE_GROUP = "e4m3", 128
 
 
 class GpuBackend:
-    """The library's kernels on one CUDA device (torch tensors in and out)."""
+    """The library's kernels on one CUDA device (torch tensors in and out), on its
+    current stream, where the exchange and the copies between the steps run too."""
 
     def __init__(self, layer: Layer):
         self.layer = layer
@@ -67,19 +69,21 @@ class GpuBackend:
         row_bytes = src[0].numel() * src.element_size() if src.shape[0] else 16
         if n:
             strata_ep_gather_rows(src.data_ptr(), rows.data_ptr(), n, src.shape[0], row_bytes,
-                                  dst.data_ptr())
+                                  dst.data_ptr(), _stream_ptr(None, src.device))
         return dst
 
     def expert_rows(self, rows, ids, n_shared, prefill, y_out, yshared_out):
         n = rows.shape[0]
         strata_moe_expert_rows(self.h, rows.data_ptr(), ids.data_ptr(), n, n_shared, prefill,
-                               y_out.data_ptr(), yshared_out.data_ptr() if n_shared else None)
+                               y_out.data_ptr(), yshared_out.data_ptr() if n_shared else None,
+                               _stream_ptr(None, rows.device))
 
     def combine(self, x, idx, w, slot, Y, prefill):
         import torch
         out = torch.empty_like(x)
         strata_moe_combine_rows(self.h, x.data_ptr(), x.shape[0], idx.data_ptr(), w.data_ptr(),
-                                slot.data_ptr(), Y.data_ptr(), prefill, out.data_ptr())
+                                slot.data_ptr(), Y.data_ptr(), prefill, out.data_ptr(),
+                                _stream_ptr(None, x.device))
         return out
 
     def y_dtype(self, prefill):

@@ -180,3 +180,108 @@ def test_plain_forward_equals_its_steps_on_bf16_rows(one_rank, shape, T):
     assert torch.equal(y, L.forward(x))
     L.sync_status()
     L.close()
+
+
+class Late:
+    """A stream whose inputs arrive late: what the calls read is written behind a
+    long wait, so a call on any other stream reads the old values."""
+
+    def __init__(self):
+        torch.cuda.synchronize()
+        self.stream = torch.cuda.Stream()
+
+    def fill(self, pairs):
+        torch.cuda._sleep(40_000_000)  # about 20 ms
+        for dst, src in pairs:
+            dst.copy_(src)
+
+
+def test_tensor_functions_follow_the_current_stream():
+    """Norm, read, routing and the layer under `torch.cuda.stream`, without a
+    stream argument: on the current stream, like the copies around them."""
+    shape, T = gen.TINY, 40
+    layer, L, sb = rule_layer(shape, T)
+    h, delta, weight = block_inputs(shape, T, 21)
+    bias = torch.from_numpy(sb).cuda()
+    rule = qe.make_routing(**RULE)
+    logits = torch.randn(T, shape.n_experts, device="cuda")
+
+    def steps(h, delta, logits):
+        h2, xn, packed = qe.add_rmsnorm(h, delta, weight, 1e-6, "e4m3", 128)
+        x = qe.dequant_rows(packed, shape.hidden)
+        idx, w = qe.route_logits(logits, rule, shape.top_k, bias)
+        y = L.forward(xn)
+        li, lw, off, lst = L.route(xn)
+        return [t.clone() for t in (h2, xn, x, idx, w, y, li, lw, off, lst)]
+
+    want = steps(h, delta, logits)
+    torch.cuda.synchronize()
+    late = Late()
+    ins = [torch.zeros_like(t) for t in (h, delta, logits)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(late.stream):
+        late.fill(zip(ins, (h, delta, logits)))
+        got = steps(*ins)
+        L.sync_status()  # waits for the current stream, too
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # a given stream, from another current one
+    for t in ins:
+        t.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(late.stream):
+        late.fill(zip(ins, (h, delta, logits)))
+    s = late.stream
+    h2, xn, packed = qe.add_rmsnorm(ins[0], ins[1], weight, 1e-6, "e4m3", 128, stream=s)
+    x = qe.dequant_rows(packed, shape.hidden, stream=s)
+    idx, w = qe.route_logits(ins[2], rule, shape.top_k, bias, stream=s)
+    y = L.forward(xn, stream=s)
+    outs = [h2, xn, x, idx, w, y, *L.route(xn, stream=s)]
+    L.sync_status(s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    L.close()
+
+
+def test_tensor_functions_join_a_capture():
+    """Inside torch.cuda.graph the calls without a stream argument are captured."""
+    shape, T = gen.TINY, 24
+    layer, L, sb = rule_layer(shape, T)
+    h, delta, weight = block_inputs(shape, T, 22)
+    ih, idl = torch.zeros_like(h), torch.zeros_like(delta)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        h2, xn, packed = qe.add_rmsnorm(ih, idl, weight, 1e-6, "int8", 32)
+        x = qe.dequant_rows(packed, shape.hidden, "int8", 32)
+        y = L.forward(xn)
+    for seed in (22, 23):
+        a, b, _ = block_inputs(shape, T, seed)
+        ih.copy_(a), idl.copy_(b)
+        g.replay()
+        rh, rxn, rp = qe.add_rmsnorm(a, b, weight, 1e-6, "int8", 32)
+        assert torch.equal(h2, rh) and torch.equal(xn, rxn) and torch.equal(x, qe.dequant_rows(rp, shape.hidden, "int8", 32))
+        assert torch.equal(y, L.forward(rxn))
+    L.sync_status()
+    del g
+    L.close()
+
+
+@pytest.mark.parametrize("T", [5, 100])
+def test_forward_block_on_a_side_stream(one_rank, T):
+    """ExpertParallel under `torch.cuda.stream`: its kernels, copies and exchange
+    stay on that stream."""
+    shape = gen.TINY
+    layer, L, sb = rule_layer(shape, T + T * shape.top_k, seed=1)
+    h, delta, weight = block_inputs(shape, T, 25)
+    ep = ExpertParallel(GpuBackend(L), shape.n_experts, shape.top_k, shape.hidden)
+    want = ep.forward_block(h, delta, weight) + (ep.forward(h),)
+    torch.cuda.synchronize()
+    ih, idl = torch.zeros_like(h), torch.zeros_like(delta)
+    for _ in range(3):
+        ih.zero_(), idl.zero_()
+        late = Late()
+        with torch.cuda.stream(late.stream):
+            late.fill([(ih, h), (idl, delta)])
+            got = ep.forward_block(ih, idl, weight) + (ep.forward(ih),)
+            L.sync_status()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    L.close()
