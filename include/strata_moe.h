@@ -314,7 +314,8 @@ strata_status strata_ep_plan(const int32_t *idx, int T, int k, int n_experts, in
 
 /* dst row i = src row rows[i] (device buffers, rows int32 [n]); row_bytes a
  * multiple of 16 and both buffers 16-byte aligned, else INVALID_ARG.  A row
- * index outside [0, n_src) is skipped.  Enqueued on `stream`. */
+ * index outside [0, n_src) is skipped.  Enqueued on `stream`; runs on the
+ * device that holds src_dev, whichever is current. */
 strata_status strata_ep_gather_rows(const void *src_dev, const int32_t *rows_dev, int n,
                                     int n_src, int row_bytes, void *dst_dev, void *stream);
 

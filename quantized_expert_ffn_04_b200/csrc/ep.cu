@@ -103,6 +103,8 @@ strata_status strata_ep_gather_rows(const void *src_dev, const int32_t *rows_dev
         (n > 0 && (!src_dev || !rows_dev || !dst_dev)))
         return STRATA_ERR_INVALID_ARG;
     if (((uintptr_t)src_dev | (uintptr_t)dst_dev) & 15) return STRATA_ERR_INVALID_ARG;
+    if (n == 0) return STRATA_OK;
+    const PointerDevice on(src_dev);  // (memory of no device: the current one launches)
     launch_gather_rows_bytes(src_dev, rows_dev, n, n_src, row_bytes, dst_dev, nullptr,
                              (cudaStream_t)stream);
     return cudaGetLastError() == cudaSuccess ? STRATA_OK : STRATA_ERR_CUDA;

@@ -86,3 +86,28 @@ def test_emulated_expert_parallel_equals_one_gpu(T, n_ranks):
         L.sync_status()
         assert np.array_equal(from_dev_bf16(outs[r]), ref), f"rank {r}: differs from one GPU"
     L.close()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_gather_runs_on_its_rows_device():
+    """Rows of a device that is not the current one."""
+    src = torch.arange(8 * 64, device="cuda:1").view(8, 64).to(torch.float32)
+    rows = torch.tensor([5, 0, 7], dtype=torch.int32, device="cuda:1")
+    dst = torch.zeros(3, 64, device="cuda:1")
+    torch.cuda.synchronize(1)
+    assert torch.cuda.current_device() == 0
+    qe.strata_ep_gather_rows(src.data_ptr(), rows.data_ptr(), 3, 8, 256, dst.data_ptr(), torch.cuda.current_stream(1).cuda_stream)
+    torch.cuda.synchronize(1)
+    assert torch.equal(dst, src[rows.long()]) and torch.cuda.current_device() == 0
+
+
+def test_gather_rows_on_a_side_stream():
+    src = torch.arange(8 * 64, device="cuda").view(8, 64).to(torch.float32)
+    rows = torch.tensor([5, 0, 7, 9, -1], dtype=torch.int32, device="cuda")
+    dst = torch.full((6, 64), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    qe.strata_ep_gather_rows(src.data_ptr(), rows.data_ptr(), 5, 8, 256, dst.data_ptr(), s.cuda_stream)
+    qe.strata_ep_gather_rows(src.data_ptr(), rows.data_ptr(), 0, 8, 256, dst.data_ptr(), s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(dst[:3], src[[5, 0, 7]]) and (dst[3:] == 7.0).all()
