@@ -642,7 +642,7 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
             }
             sum += s[q];
         }
-        float f = p.scale;
+        float f = 1.0f;
         if (p.renorm) {
             sum = lanes_sum<S>(sum);
             const bool tiny = sum < 0x1p-60f && n;
@@ -660,13 +660,13 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
                 }
                 sum = lanes_sum<S>(sum);
             }
-            f = __fdividef(p.scale, sum);
+            f = __fdividef(1.0f, sum);
         }
 #pragma unroll
         for (int q = 0; q < kPicks; q++)
             if (r + q * S < p.k && n && live) {
                 idx[t * p.k + r + q * S] = e[q];
-                w[t * p.k + r + q * S] = s[q] * f;
+                w[t * p.k + r + q * S] = s[q] * f * p.scale;  // scale / sum may leave fp32's range
             }
         __syncwarp();  // the scratch is free for the warp's next tokens
     }

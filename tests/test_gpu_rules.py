@@ -633,3 +633,20 @@ def test_extreme_logits_with_a_bias(T):
                     assert np.array_equal(idx[sample], ridx), (kw, name, sample[np.any(idx[sample] != ridx, axis=1)])
                     np.testing.assert_allclose(w[sample], rw, rtol=W_TOL if score == "sigmoid" or renorm else W_TOL_PLAIN_SOFTMAX,
                                                atol=1e-37)
+
+
+@pytest.mark.parametrize("T", [5, 9001, 17001])
+def test_any_scale(T):
+    """Factors near either end of fp32's range, with scores that sum to little."""
+    E, k = 64, 4
+    l = logits_of(T, E, 95)
+    l[1::2] -= 40
+    sample = np.unique(np.r_[0:min(T, 30), max(0, T - 30):T])
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, bias_of(E, 96, 0.2 / E)):
+            for scale in (3e38, 1e25, -1e25, 1e-30, 0.0):
+                kw = dict(score=score, scale=scale)
+                idx, w = call(l, k, bias, **kw)
+                ridx, rw = route_rule(l[sample], k, bias=bias, **dict(kw, scale=float(np.float32(scale))))
+                assert np.array_equal(idx[sample], ridx)
+                np.testing.assert_allclose(w[sample], rw, rtol=W_TOL, atol=1e-37)
