@@ -451,7 +451,13 @@ class Layer:
         strata_moe_set_option(self.handle, option, value)
 
     def set_routing(self, rule=None, select_bias=None):
-        """Pick and weigh by `rule` (make_routing) from now on; None: the default."""
+        """Pick and weigh by `rule` (make_routing) from now on; None: the default.
+        select_bias: n_experts floats on the host, or None."""
+        import numpy as np
+        if select_bias is not None:
+            select_bias = np.ascontiguousarray(select_bias, dtype=np.float32)
+            if select_bias.shape != (self.shape.n_experts,):
+                raise ValueError(f"select_bias must have {self.shape.n_experts} values")
         strata_moe_set_routing(self.handle, rule, select_bias)
 
     def forward(self, x, out=None, stream=None):

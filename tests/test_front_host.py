@@ -145,3 +145,23 @@ def test_tensor_functions_refuse_host_tensors():
         with pytest.raises(ValueError):
             bad()
     assert qe.packed_row_bytes(2560) == 2640 and qe.packed_row_bytes(256, 0) == 272 and qe.packed_row_bytes(6144, 32) == 6912
+
+
+def test_layer_set_routing_refuses_a_bias_of_another_length(monkeypatch):
+    """The C call copies n_experts floats from the host: fewer would be read past
+    their end."""
+    import gen
+    L = object.__new__(qe.Layer)
+    L.handle, L.shape = None, gen.TINY
+    seen = []
+    monkeypatch.setattr(qe, "strata_moe_set_routing", lambda *a: seen.append(a))
+    E = gen.TINY.n_experts
+    for bad in (np.zeros(E - 1), np.zeros(E + 1), np.zeros((E, 2)), np.zeros((1, E)), 0.5, np.zeros(0)):
+        with pytest.raises(ValueError, match=f"{E} values"):
+            L.set_routing(rule(), bad)
+    assert not seen
+    L.set_routing(rule(), [0.0] * E)
+    L.set_routing(rule(), np.zeros(E, np.float64)[::-1])
+    L.set_routing(rule())
+    L.set_routing()
+    assert len(seen) == 4 and seen[1][2].shape == (E,) and seen[2][2] is None
