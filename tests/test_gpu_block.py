@@ -285,3 +285,14 @@ def test_forward_block_on_a_side_stream(one_rank, T):
             L.sync_status()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
     L.close()
+
+
+def test_forward_block_without_tokens(one_rank):
+    shape = gen.TINY
+    layer, L, sb = rule_layer(shape, 8, seed=1)
+    ep = ExpertParallel(GpuBackend(L), shape.n_experts, shape.top_k, shape.hidden)
+    none = torch.empty(0, shape.hidden, dtype=torch.bfloat16, device="cuda")
+    h, y = ep.forward_block(none, none, None)
+    assert h.shape == y.shape == none.shape and ep.forward(none).shape == none.shape
+    L.sync_status()
+    L.close()

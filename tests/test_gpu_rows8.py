@@ -414,3 +414,26 @@ def test_rows_over_the_whole_range(q8, group, wt, eps):
     torch.cuda.synchronize()
     _, y = norm_rows(f64(x), None, None, eps)
     assert (np.abs(f64(n.xn[:T]) - y) <= (2.0 ** -8 + FP32_TOL) * np.abs(y) + 2.0 ** -134 + 2.0 ** -149).all()
+
+
+def test_norm_rows_past_32_bits():
+    """Rows further than 2^32 bytes into x, xn and the codes: as in a call of their own."""
+    H = 16384
+    T = (1 << 32) // H + 5  # one byte a code
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    tail, _, w = inputs(5, H, 41, torch.float32)
+    x[-5:] = tail
+    xn = torch.empty_like(x)
+    q = torch.empty((T, H), dtype=torch.uint8, device="cuda")
+    scale = torch.empty((T, H // 32), device="cuda")
+
+    def go(x, n, xn, q, scale):
+        qe.strata_moe_add_rmsnorm(x.data_ptr(), None, w.data_ptr(), qe.STRATA_F32, 1e-6, n, H, None, xn.data_ptr(), qe.STRATA_Q8_E4M3, 32,
+                                  q.data_ptr(), H, scale.data_ptr(), H // 32)
+
+    go(x, T, xn, q, scale)
+    few = [torch.empty_like(t[:5]) for t in (xn, q, scale)]
+    go(tail, 5, *few)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[-5:], b) for a, b in zip((xn, q, scale), few))
+    assert (xn[:-5] == 0).all() and (q[:-5] == 0).all() and (scale[:-5] == 0).all()

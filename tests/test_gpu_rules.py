@@ -650,3 +650,18 @@ def test_any_scale(T):
                 ridx, rw = route_rule(l[sample], k, bias=bias, **dict(kw, scale=float(np.float32(scale))))
                 assert np.array_equal(idx[sample], ridx)
                 np.testing.assert_allclose(w[sample], rw, rtol=W_TOL, atol=1e-37)
+
+
+@pytest.mark.parametrize("T", [1100, 8200])
+def test_logits_past_32_bits(T):
+    """Rows of logits that lie further than 2^32 bytes from the first."""
+    E, k = 64, 6
+    ld = (1 << 30) // (T - 20) // 4 * 4 + 4
+    l = logits_of(T, E, 99)
+    flat = torch.zeros((T - 1) * ld + E, device="cuda")
+    view = flat.as_strided((T, E), (ld, 1))
+    view.copy_(torch.from_numpy(l))
+    assert (T - 1) * ld * 4 > 1 << 32
+    idx, w = call(view, k, bias_of(E, 4), score="sigmoid")
+    i2, w2 = call(l, k, bias_of(E, 4), score="sigmoid")
+    assert np.array_equal(idx, i2) and np.array_equal(w, w2)
