@@ -238,9 +238,9 @@ enum { STRATA_Q8_E4M3 = 0, STRATA_Q8_INT8 = 1 };
  *              past H and scales past the row's groups are left as they are,
  *              so codes and scales may share one packed row of
  *              q_stride = 4 * scale_stride bytes.
- * Squares are summed in fp32, in 64 bits when the sum leaves its range.  H a multiple of 32 up to 16384; pointers
- * 16-byte aligned (scale_dev and a float weight_dev included), q_stride a
- * multiple of 16; eps >= 0.  Other overlaps of outputs with anything are
+ * Squares are summed in fp32, in 64 bits when the sum leaves its range.
+ * H a multiple of 32 up to 16384; pointers 16-byte aligned (scale_dev and a float
+ * weight_dev included), q_stride a multiple of 16; eps >= 0.  Other overlaps of outputs with anything are
  * refused.  Runs on the device that holds x_dev; no workspace. */
 strata_status strata_moe_add_rmsnorm(const void *x_dev, const void *delta_dev,
                                      const void *weight_dev, int weight_type, float eps, int T,
@@ -398,7 +398,8 @@ strata_status strata_moe_selftest_wait(int device, int64_t budget_cycles);
  * (for T > 256: the fp16 token copy, the screening GEMM and the screened
  * top-k), 1 top-k + dispatch (T <= 256, one kernel), 2 dispatch (T > 256),
  * 3 gate/up + SwiGLU (on the prefill path with T <= 256 also the fp16 token
- * copy), 4 down, 5 combine.  NULL events
+ * copy), 4 down, 5 combine.  With a routing rule: 0 the exact router, 1 (T <= 256)
+ * or 2 the rule and the dispatch.  NULL events
  * switch the probe off.  The events must be created by the caller on the
  * handle's device (with timing enabled); forwards captured into a CUDA graph
  * capture the event records too. */

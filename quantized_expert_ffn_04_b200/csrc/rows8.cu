@@ -6,10 +6,10 @@
 //   code = round(y M / max|y|);  read back: bf16(code s).
 //
 // Both kernels are one pass over HBM, which bounds them at prompt sizes: 8192 rows
-// of 2560 (x, delta in; h, xn, e4m3 codes out: 189 MB) 30.6 us back to back where a
-// copy's rate gives 28.9, 81920 rows read (441 MB, 420 of them written) 64 us where
-// a fill of the output takes 60; with inputs that left L2 33 and 75 us.  One to 64
-// rows take 2.2 to 2.5 us, a launch.
+// of 2560 (x, delta in; h, xn, e4m3 codes out: 189 MB) 33 us, with inputs that left
+// L2, where a copy's rate gives 28.9; 81920 rows read (441 MB, 420 of them written)
+// 74 us where it gives 67 (64 back to back, a fill of the output alone 60).  One to
+// 64 rows take 2.2 to 2.5 us, a launch.
 #include <float.h>
 #include <math.h>
 
@@ -123,8 +123,8 @@ __device__ __forceinline__ float row_max(float v, float *scratch) {
 // One row a block; thread i holds the 16-byte vectors i and (NV == 2)
 // i + blockDim.x, so that the row stays in registers between its one read and its
 // one write (a warp a row needs 10 vectors a thread: 46 to 58 us for 8192 rows of
-// 2560).  255 instructions a vector; the issue slots are 71 % taken.  kGroup: columns a scale covers, 0 for the whole row, -1 for
-// no 8-bit output.
+// 2560).  261 instructions a vector; the issue slots are 72 % taken.  kGroup: columns
+// a scale covers, 0 for the whole row, -1 for no 8-bit output.
 template <int NV, int kQ8, int kGroup, bool kF32Weight>
 __global__ __launch_bounds__(kNormThreads) void add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float fs[64], ms[32];

@@ -2,10 +2,12 @@
 // the same kernel for a layer whose rule is set (strata_moe_set_routing).
 //
 // One warp per token here, several tokens a warp in select_batch.cu (select.cuh).
-// The work is one read of the logits and a few hundred instructions a token; the
-// instructions bound it: 65536 tokens of 256 experts (8 groups, sigmoid scores
-// with a bias) take 39 us, about 470 instructions a token at 66 % of the issue slots,
-// where the read alone would take 11; without groups and bias 23 us.
+// The work is one read of the logits and a few hundred instructions a token.  In
+// large batches the instructions bound it: 65536 tokens of 256 experts (8 groups,
+// sigmoid scores with a bias) take 39 us, 481 instructions a token at 74 % of the
+// issue slots, where the read alone would take 11; without groups and bias 20.6 us.
+// With a token a warp it is the loads' latency first: 8192 tokens of 512 experts
+// (sigmoid, bias) take 8.7 us at 57 % of the issue slots (the read: 2.7).
 #include <math.h>
 
 #include "common.cuh"

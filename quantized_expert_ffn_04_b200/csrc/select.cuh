@@ -688,10 +688,11 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
 template <int S>
 constexpr int kSelectWarps = S == 32 ? 4 : 8;
 // Blocks an SM holds at least (a bound on registers).  Batches: 64 registers
-// (65536 tokens of 256 experts, 16 lanes each: 39 us, 46 without the bound).  A
-// token a warp: 72 (8192 tokens of 512: 10.2 us against 11.7); softmax values with
-// a bias, which would spill there, 96 (1037 tokens of 512: 4.8 us, 5.9 with 72;
-// 8192: 11.6, 13.6 without the bound).
+// (65536 tokens of 256 experts, 16 lanes each: 38.7 us, 52.6 without the bound;
+// without groups and bias 20.6 and 26.0).  A token a warp: 72 (8192 tokens of 512:
+// 8.8 us against 10.3); softmax values with a bias, which would spill there, 96
+// (1037 tokens of 512: 4.6 us, 8.4 with 72 and 4.6 without a bound; 8192: 14.4,
+// 14.8 and 13.7).
 template <int S, int NQ, bool kSpills>
 constexpr int kSelectBlocks = S < 32 ? 4 : NQ > 32 ? 2 : NQ > 16 ? 4 : kSpills ? 5 : 7;
 

@@ -17,16 +17,20 @@ the router and the shared expert.  A forward of the rank's own T tokens:
 Each expert output depends on one token row and one expert only, and the
 combine is the one-GPU combine on the same values, so the result is the same
 bits as the one-GPU forward of the rank's tokens on the same kernels (the
-decode GEMV chain up to 64 tokens, the tensor-core prefill above; the fused
-decode kernel sums its K partials in another order and agrees within the
-layer tolerance).  The exchange is
-torch.distributed's all_to_all_single (NCCL on GPUs, gloo on CPU).
+decode GEMV chain while no rank has more than 64 tokens, the tensor-core prefill
+on every rank otherwise; the fused decode kernel sums its K partials in another
+order and agrees within the layer tolerance).  The exchange is
+torch.distributed's all_to_all_single (NCCL on GPUs, gloo on CPU), on the same
+stream as the kernels.
 
 ExpertParallel.forward_block starts a step earlier, at the block's pre-norm
 (strata_moe_add_rmsnorm), and exchanges the normalised rows in 8 bits with
 scales, half of the bf16 bytes: every expert, routed or shared, runs on the
-rows read back from 8 bits (strata_moe_dequant_rows), so that all ranks see the
-same row (its prescale exponent included); the router sees the bf16 rows.
+rows read back from 8 bits (strata_moe_dequant_rows).  The shared expert's rows do
+not travel, but the combine scales all of a token's outputs by the prescale
+exponent of one row, which has to be the row that the owners ran; a result also
+does not depend on how many ranks share the experts.  The router sees the bf16
+rows.
 
 The compute steps go through a backend; GpuBackend calls the library's
 kernels through the C ABI.  Any object with the same methods works (the
