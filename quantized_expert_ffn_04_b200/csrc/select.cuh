@@ -622,9 +622,10 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
                 __syncwarp();
             }
         }
-        // picks r, r + S, ... and their weights, of which the sum is taken
-        // relative to the largest pick where it would leave fp32's normal range (for
-        // that token alone: a token's weights do not depend on the warp's others)
+        // picks r, r + S, ... and their weights, which are taken relative to the
+        // largest pick where they sum to less than 2^-20 (for that token alone: a
+        // token's weights do not depend on the warp's others), so that a score below
+        // fp32's normal range belongs to a weight below 2^-106
         constexpr int kPicks = S < 32 ? 16 / S : 1;  // k <= 16 there
         float l[kPicks], s[kPicks], sum = 0.0f;
         int e[kPicks];
@@ -645,7 +646,7 @@ __device__ __forceinline__ void select_tokens(const SelectPlan &p, const void *l
         float f = 1.0f;
         if (p.renorm) {
             sum = lanes_sum<S>(sum);
-            const bool tiny = sum < 0x1p-60f && n;
+            const bool tiny = sum < 0x1p-20f && n;
             if (__any_sync(kAll, tiny)) {
                 float top = -INFINITY;
 #pragma unroll

@@ -665,3 +665,26 @@ def test_logits_past_32_bits(T):
     idx, w = call(view, k, bias_of(E, 4), score="sigmoid")
     i2, w2 = call(l, k, bias_of(E, 4), score="sigmoid")
     assert np.array_equal(idx, i2) and np.array_equal(w, w2)
+
+
+@pytest.mark.parametrize("T", [3, 9001, 17001])
+def test_small_weights_next_to_small_sums(T):
+    """Renormalised weights keep their relative accuracy where the picks' scores sum
+    to little and differ by many powers of two (down to 2^-106 of the sum, where
+    scores leave fp32's normal range: 1e-31 covers it)."""
+    E, k = 64, 5
+    l = np.full((T, E), -300, np.float32)
+    rng = np.random.default_rng(98)
+    step = np.log(2) * np.array([0, -25, -50, -70, -85])
+    for t in range(T):
+        l[t, 10:15] = step - (t % 62) * np.log(2) - rng.random(5)
+    bias = np.full(E, -4.0, np.float32)
+    bias[10:15] = [0.5, 0.4, 0.3, 0.2, 0.1]
+    soft = l.copy()
+    soft[:, 40] = 0.5  # takes nearly all of the softmax and is not picked
+    sample = np.unique(np.r_[0:min(T, 62), max(0, T - 62):T])
+    for score, rows, b in (("softmax", soft, bias), ("sigmoid", l, bias), ("sigmoid", l, None)):
+        idx, w = call(rows, k, b, score=score)
+        ridx, rw = route_rule(rows[sample], k, bias=b, score=score)
+        assert np.array_equal(idx[sample], ridx)
+        np.testing.assert_allclose(w[sample], rw, rtol=2 * W_TOL, atol=1e-31)
